@@ -33,6 +33,8 @@ EXPORTS = ('gdn2_set_stream', 'gdn2_get_stream', 'gdn2_status_string',
            'gdn2_decode_step', 'gdn2_decode_step_gates',
            'gdn2_chunk_fwd_prologue', 'gdn2_decode_step_prologue',
            'gdn2_chunk_bwd_workspace_bytes', 'gdn2_chunk_bwd', 'gdn2_chunk_fwd_keep', 'gdn2_chunk_bwd_kept',
+           'gdn2_recurrent_fwd', 'gdn2_prologue_fwd', 'gdn2_prologue_bwd_workspace_bytes', 'gdn2_prologue_bwd',
+           'gdn2_layer_norm_fwd', 'gdn2_layer_norm_bwd_workspace_bytes', 'gdn2_layer_norm_bwd',
            'gdn2_profile_begin', 'gdn2_profile_end', 'gdn2_profile_kernel')
 
 
@@ -89,6 +91,21 @@ def _load() -> ctypes.CDLL:
     lib.gdn2_chunk_fwd_keep.restype = i
     lib.gdn2_chunk_bwd_kept.argtypes = [vp] * 10 + [i] * 7 + [vp] * 7 + [vp, sz]
     lib.gdn2_chunk_bwd_kept.restype = i
+    i64, f = ctypes.c_int64, ctypes.c_float
+    lib.gdn2_recurrent_fwd.argtypes = [vp] * 6 + [i] + [vp] * 6 + [i] * 10
+    lib.gdn2_recurrent_fwd.restype = i
+    lib.gdn2_prologue_fwd.argtypes = [vp] * 5 + [i, pc] + [vp] * 9 + [i] * 9
+    lib.gdn2_prologue_fwd.restype = i
+    lib.gdn2_prologue_bwd_workspace_bytes.argtypes = [i] * 8
+    lib.gdn2_prologue_bwd_workspace_bytes.restype = sz
+    lib.gdn2_prologue_bwd.argtypes = [vp] * 5 + [i, pc] + [vp] * 18 + [i] * 10 + [vp, sz]
+    lib.gdn2_prologue_bwd.restype = i
+    lib.gdn2_layer_norm_fwd.argtypes = [vp] * 6 + [i64, i, f, i, i]
+    lib.gdn2_layer_norm_fwd.restype = i
+    lib.gdn2_layer_norm_bwd_workspace_bytes.argtypes = [i64, i]
+    lib.gdn2_layer_norm_bwd_workspace_bytes.restype = sz
+    lib.gdn2_layer_norm_bwd.argtypes = [vp] * 7 + [i64, i, f, i, i, vp, sz]
+    lib.gdn2_layer_norm_bwd.restype = i
     lib.gdn2_profile_begin.argtypes = [i]
     lib.gdn2_profile_begin.restype = i
     lib.gdn2_profile_end.argtypes = []
@@ -518,3 +535,301 @@ def chunk_bwd_kept(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha:
     left in ``workspace`` (gdn2_chunk_bwd_kept): the same gradients without
     running the forward again."""
     return _bwd('gdn2_chunk_bwd_kept', q, k, v, log_alpha, b, w, S0, dO, dST, cu_seqlens, workspace, True)
+
+
+# ---- operators around the mixer: the recurrence on state slots, the prologue
+# and the closing layer norm. Their tensors live on one GPU, which need not be
+# the current one; work goes to that GPU's current stream.
+
+_CODES = {torch.float32: GDN2_F32, torch.bfloat16: GDN2_BF16}
+
+
+def _gpu(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f'{name}: must be on the GPU, got {t.device}')
+    return t.device
+
+
+def _need(t: torch.Tensor, name: str, shape, dtype, device):
+    """_check, with its messages, at the cost of one comparison each where all is well."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _check(t, name, shape, dtype, device)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, where: str, dev: torch.device, *args) -> None:
+    """Call the library on ``dev``'s current stream, with ``dev`` current."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _call(fn, where, dev, *args)
+    _lib.gdn2_set_stream(torch.cuda.current_stream(dev).cuda_stream)
+    st = fn(*args)
+    if st != GDN2_OK:
+        raise Gdn2Error(st, where)
+
+
+def _index(t: Optional[torch.Tensor], name: str, n: int, dev):
+    if t is not None:
+        _need(t, name, (n,), torch.int32, dev)
+
+
+def _gate(t: torch.Tensor, name: str, shape, dtype, dev, bit: int) -> int:
+    """Layout bit of a gate: 0 with its channel axis, ``bit`` without."""
+    if t.dim() == len(shape):
+        _need(t, name, shape, dtype, dev)
+        return 0
+    _need(t, name, shape[:-1], dtype, dev)
+    return bit
+
+
+def _heads(q, k, v, cu_seqlens, names):
+    """Sizes from q, k [B, T, HK, dk] and v [B, T, H, dv], checked."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f'{names[0]} and {names[2]} must be [B, T, heads, d]')
+    dev, dt = _gpu(q, names[0]), q.dtype
+    _dtype_code(q)
+    B, T, HK, dk = q.shape
+    H, dv = v.shape[2:]
+    _need(k, names[1], q.shape, dt, dev)
+    _need(q, names[0], q.shape, dt, dev)
+    _need(v, names[2], (B, T, H, dv), dt, dev)
+    if HK < 1 or H % HK:
+        raise ValueError(f'{names[2]}: its {H} heads are not a multiple of the {HK} of {names[0]}')
+    return dev, dt, B, T, _seq_count(cu_seqlens, B, dev), H, HK, dk, dv
+
+
+def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: torch.Tensor, b: torch.Tensor,
+                  w: torch.Tensor, state: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, *,
+                  slot_in: Optional[torch.Tensor] = None, slot_out: Optional[torch.Tensor] = None,
+                  commit: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The recurrence token by token over short sequences, their states in a pool
+    (gdn2_recurrent_fwd): continuous batching, draft tokens, short prompts.
+
+    q, k: [B, T, HK, dk]; v: [B, T, H, dv] (bf16 or fp32; HK divides H, head h
+    uses q/k head h // (H // HK)); b, log_alpha: [B, T, H, dk] and w:
+    [B, T, H, dv], or [B, T, H] for one gate per token-head (log_alpha fp32).
+    With ``cu_seqlens`` B is 1 and the sequences are packed along T.
+    state: [slots, H, dk, dv] fp32, updated in place. slot_in, slot_out, commit:
+    int32 [N] on the device, as gdn2.h has them (slot numbers outside the pool:
+    zeros in, not kept; commit: leading tokens whose effect is kept). Returns
+    o [B, T, H, dv] in ``out_dtype`` (fp32 or bf16)."""
+    dev, dt, B, T, N, H, HK, dk, dv = _heads(q, k, v, cu_seqlens, ('q', 'k', 'v'))
+    lead = (B, T, H)
+    gates = (_gate(b, 'b', (*lead, dk), dt, dev, GDN2_GATE_B_PER_HEAD)
+             | _gate(w, 'w', (*lead, dv), dt, dev, GDN2_GATE_W_PER_HEAD)
+             | _gate(log_alpha, 'log_alpha', (*lead, dk), torch.float32, dev, GDN2_GATE_ALPHA_PER_HEAD))
+    if state.dim() != 4:
+        raise ValueError('state must be [slots, H, dk, dv]')
+    slots = state.shape[0]
+    _need(state, 'state', (slots, H, dk, dv), torch.float32, dev)
+    _index(slot_in, 'slot_in', N, dev)
+    _index(slot_out, 'slot_out', N, dev)
+    _index(commit, 'commit', N, dev)
+    if slot_in is None and slots < N:
+        raise ValueError(f'state: {slots} slots for {N} sequences (pass slot_in)')
+    if out is None:
+        if out_dtype not in _CODES:
+            raise TypeError(f'unsupported output dtype {out_dtype} (bfloat16 or float32)')
+        out = torch.empty((B, T, H, dv), dtype=out_dtype, device=dev)
+    else:
+        if out.dtype not in _CODES:
+            raise TypeError(f'unsupported output dtype {out.dtype} (bfloat16 or float32)')
+        _need(out, 'out', (B, T, H, dv), out.dtype, dev)
+    _call(_lib.gdn2_recurrent_fwd, 'gdn2_recurrent_fwd', dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_alpha.data_ptr(), b.data_ptr(), w.data_ptr(), gates, state.data_ptr(), _addr(slot_in), _addr(slot_out),
+          _addr(commit), out.data_ptr(), _addr(cu_seqlens), B, T, N, H, HK, slots, dk, dv, _CODES[dt],
+          _CODES[out.dtype])
+    return out
+
+
+def _conv_pools(conv_weight, conv_bias, conv_state, conv_state_out, heads, dims, dt, dev):
+    """ShortConv of a prologue call whose histories are pools, and their slots."""
+    sc = ShortConv()
+    if conv_weight is None or len(conv_weight) != 3:
+        raise ValueError('conv_weight must be a (q, k, v) triple of [heads*d, 4] float32 tensors')
+    slots = 0
+    for n, t, h, d in zip('qkv', conv_weight, heads, dims):
+        _need(t, f'conv_weight[{n}]', (h * d, 4), torch.float32, dev)
+        setattr(sc, f'weight_{n}', t.data_ptr())
+    if conv_bias is not None:
+        for n, t, h, d in zip('qkv', conv_bias, heads, dims):
+            if t is not None:
+                _need(t, f'conv_bias[{n}]', (h * d,), torch.float32, dev)
+                setattr(sc, f'bias_{n}', t.data_ptr())
+    for label, trip in (('in', conv_state), ('out', conv_state_out)):
+        if trip is None:
+            continue
+        if len(trip) != 3:
+            raise ValueError('conv_state must be a (q, k, v) triple')
+        for n, t, h, d in zip('qkv', trip, heads, dims):
+            slots = slots or t.shape[0]
+            _need(t, f'conv_state_{label}[{n}]', (slots, h, 3, d), dt, dev)
+            setattr(sc, f'state_{label}_{n}', t.data_ptr())
+    return sc, slots
+
+
+def _prologue_sizes(q_raw, k_raw, v_raw, b_logit, w_logit, cu_seqlens):
+    dev, dt, B, T, N, H, HK, dk, dv = _heads(q_raw, k_raw, v_raw, cu_seqlens, ('q_raw', 'k_raw', 'v_raw'))
+    gates = (_gate(b_logit, 'b_logit', (B, T, H, dk), dt, dev, GDN2_GATE_B_PER_HEAD)
+             | _gate(w_logit, 'w_logit', (B, T, H, dv), dt, dev, GDN2_GATE_W_PER_HEAD))
+    return dev, dt, gates, B, T, N, H, HK, dk, dv
+
+
+def prologue_fwd(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor, b_logit: torch.Tensor,
+                 w_logit: torch.Tensor, conv_weight, conv_bias=None, cu_seqlens: Optional[torch.Tensor] = None, *,
+                 conv_state=None, conv_state_out=None, slot_in: Optional[torch.Tensor] = None,
+                 slot_out: Optional[torch.Tensor] = None, commit: Optional[torch.Tensor] = None, out=None):
+    """The mixer's inputs from the layer's projections (gdn2_prologue_fwd): q and
+    k through their short convolutions and to unit norm, v through its own,
+    b and w through the sigmoid.
+
+    q_raw, k_raw: [B, T, HK, dk]; v_raw: [B, T, H, dv]; b_logit: [B, T, H, dk] or
+    [B, T, H]; w_logit: [B, T, H, dv] or [B, T, H]. conv_weight, conv_bias as in
+    ``chunk_fwd_prologue`` (q and k: HK*dk channels). conv_state,
+    conv_state_out: (q, k, v) pools of histories, [slots, HK, 3, dk] twice and
+    [slots, H, 3, dv], or None for zeros / not written; conv_state_out may be
+    conv_state itself. slot_in, slot_out, commit as in ``recurrent_fwd``. out:
+    five tensors to write, or None. Returns (q, k, v, b, w) in the input dtype."""
+    dev, dt, gates, B, T, N, H, HK, dk, dv = _prologue_sizes(q_raw, k_raw, v_raw, b_logit, w_logit, cu_seqlens)
+    sc, slots = _conv_pools(conv_weight, conv_bias, conv_state, conv_state_out, (HK, HK, H), (dk, dk, dv), dt, dev)
+    _index(slot_in, 'slot_in', N, dev)
+    _index(slot_out, 'slot_out', N, dev)
+    _index(commit, 'commit', N, dev)
+    if slots and slot_in is None and slots < N:
+        raise ValueError(f'conv_state: {slots} slots for {N} sequences (pass slot_in)')
+    raw = (q_raw, k_raw, v_raw, b_logit, w_logit)
+    if out is None:
+        out = tuple(torch.empty_like(x) for x in raw)
+    else:
+        if len(out) != 5:
+            raise ValueError('out must be (q, k, v, b, w)')
+        for n, t, x in zip('qkvbw', out, raw):
+            _need(t, f'out[{n}]', x.shape, dt, dev)
+    _call(_lib.gdn2_prologue_fwd, 'gdn2_prologue_fwd', dev, *(x.data_ptr() for x in raw), gates, ctypes.byref(sc),
+          _addr(slot_in), _addr(slot_out), _addr(commit), *(x.data_ptr() for x in out), _addr(cu_seqlens), B, T, N, H,
+          HK, slots, dk, dv, _CODES[dt])
+    return tuple(out)
+
+
+def prologue_bwd(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor, b_logit: torch.Tensor,
+                 w_logit: torch.Tensor, conv_weight, conv_bias, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
+                 db: torch.Tensor, dw: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, *, conv_state=None,
+                 slot_in: Optional[torch.Tensor] = None, grad_dtype: Optional[torch.dtype] = None,
+                 workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradient of ``prologue_fwd`` (gdn2_prologue_bwd) from dq, dk, dv, db, dw,
+    fp32 and shaped like q, k, v, b, w (what ``chunk_bwd`` returns). Returns
+    {'q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit'} in ``grad_dtype`` (None:
+    the inputs'), fp32 {'weight_q', 'weight_k', 'weight_v'} [heads*d, 4] and
+    'bias_q', 'bias_k', 'bias_v' for the biases that conv_bias holds."""
+    dev, dt, gates, B, T, N, H, HK, Dk, Dv = _prologue_sizes(q_raw, k_raw, v_raw, b_logit, w_logit, cu_seqlens)
+    heads, dims = (HK, HK, H), (Dk, Dk, Dv)
+    sc, slots = _conv_pools(conv_weight, conv_bias, conv_state, None, heads, dims, dt, dev)
+    _index(slot_in, 'slot_in', N, dev)
+    if slots and slot_in is None and slots < N:
+        raise ValueError(f'conv_state: {slots} slots for {N} sequences (pass slot_in)')
+    raw, grads = (q_raw, k_raw, v_raw, b_logit, w_logit), (dq, dk, dv, db, dw)
+    for n, t, x in zip(('dq', 'dk', 'dv', 'db', 'dw'), grads, raw):
+        _need(t, n, x.shape, torch.float32, dev)
+    grad_dtype = dt if grad_dtype is None else grad_dtype
+    if grad_dtype not in _CODES:
+        raise TypeError(f'unsupported gradient dtype {grad_dtype} (bfloat16 or float32)')
+    g = {n: torch.empty(x.shape, dtype=grad_dtype, device=dev)
+         for n, x in zip(('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit'), raw)}
+    for n, h, d in zip('qkv', heads, dims):
+        g['weight_' + n] = torch.empty((h * d, 4), dtype=torch.float32, device=dev)
+    for z, (n, h, d) in enumerate(zip('qkv', heads, dims)):
+        if conv_bias is not None and conv_bias[z] is not None:
+            g['bias_' + n] = torch.empty((h * d,), dtype=torch.float32, device=dev)
+    need = _lib.gdn2_prologue_bwd_workspace_bytes(B, T, N, H, HK, Dk, Dv, int(cu_seqlens is not None))
+    if need == 0:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, 'gdn2_prologue_bwd_workspace_bytes')
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f'workspace: must be contiguous on {dev}')
+    _call(_lib.gdn2_prologue_bwd, 'gdn2_prologue_bwd', dev, *(x.data_ptr() for x in raw), gates, ctypes.byref(sc),
+          _addr(slot_in), *(x.data_ptr() for x in grads),
+          *(g[n].data_ptr() for n in ('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit')),
+          *(g['weight_' + n].data_ptr() for n in 'qkv'), *(_addr(g.get('bias_' + n)) for n in 'qkv'),
+          _addr(cu_seqlens), B, T, N, H, HK, slots, Dk, Dv, _CODES[dt], _CODES[grad_dtype], workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return g
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, *, eps: float = 1e-5, output_sum: bool = False,
+                   out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None):
+    """LayerNorm(x + residual) over the last axis (gdn2_layer_norm_fwd). x,
+    residual: [..., cols], one dtype (bf16 or fp32); weight, bias: [cols] fp32.
+    Returns (y in ``out_dtype`` (None: x's), h or None): h = x + residual, what
+    ``layer_norm_bwd`` takes, with ``output_sum`` or into ``sum_out`` (which,
+    like ``out``, may be x or residual itself)."""
+    dev, dt, shape = _gpu(x, 'x'), x.dtype, x.shape
+    _dtype_code(x)
+    if x.dim() < 1 or shape[-1] < 1:
+        raise ValueError('x must be [..., cols] with cols >= 1')
+    cols = shape[-1]
+    _need(x, 'x', shape, dt, dev)
+    _need(weight, 'weight', (cols,), torch.float32, dev)
+    if bias is not None:
+        _need(bias, 'bias', (cols,), torch.float32, dev)
+    if residual is not None:
+        _need(residual, 'residual', shape, dt, dev)
+    if sum_out is not None:
+        _need(sum_out, 'sum_out', shape, dt, dev)
+    elif output_sum:
+        sum_out = torch.empty_like(x)
+    out_dtype = out.dtype if out is not None else (dt if out_dtype is None else out_dtype)
+    if out_dtype not in _CODES:
+        raise TypeError(f'unsupported output dtype {out_dtype} (bfloat16 or float32)')
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        _need(out, 'out', shape, out_dtype, dev)
+    _call(_lib.gdn2_layer_norm_fwd, 'gdn2_layer_norm_fwd', dev, x.data_ptr(), _addr(residual), weight.data_ptr(),
+          _addr(bias), out.data_ptr(), _addr(sum_out), x.numel() // cols, cols, eps, _CODES[dt], _CODES[out_dtype])
+    return out, sum_out
+
+
+def layer_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, *, dsum: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradient of ``layer_norm_fwd`` (gdn2_layer_norm_bwd). h: [..., cols], the
+    sum the forward returned (x where there was no residual); dy: shaped like
+    it, bf16 or fp32; dsum: a further gradient of h, added on. Returns
+    {'x': dL/dh (of x and of residual alike) in h's dtype, 'weight', 'bias':
+    fp32 [cols]}."""
+    dev, dt, shape = _gpu(h, 'h'), h.dtype, h.shape
+    _dtype_code(h)
+    if h.dim() < 1 or shape[-1] < 1:
+        raise ValueError('h must be [..., cols] with cols >= 1')
+    cols = shape[-1]
+    rows = h.numel() // cols
+    if dy.dtype not in _CODES:
+        raise TypeError(f'unsupported gradient dtype {dy.dtype} (bfloat16 or float32)')
+    _need(h, 'h', shape, dt, dev)
+    _need(dy, 'dy', shape, dy.dtype, dev)
+    _need(weight, 'weight', (cols,), torch.float32, dev)
+    if dsum is not None:
+        _need(dsum, 'dsum', shape, dt, dev)
+    if out is None:
+        out = torch.empty_like(h)
+    else:
+        _need(out, 'out', shape, dt, dev)
+    g = {'x': out, 'weight': torch.empty_like(weight), 'bias': torch.empty_like(weight)}
+    need = _lib.gdn2_layer_norm_bwd_workspace_bytes(rows, cols)
+    if need == 0:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, 'gdn2_layer_norm_bwd_workspace_bytes')
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f'workspace: must be contiguous on {dev}')
+    _call(_lib.gdn2_layer_norm_bwd, 'gdn2_layer_norm_bwd', dev, dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
+          _addr(dsum), out.data_ptr(), g['weight'].data_ptr(), g['bias'].data_ptr(), rows, cols, eps, _CODES[dt],
+          _CODES[dy.dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return g

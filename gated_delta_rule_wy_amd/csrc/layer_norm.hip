@@ -1,0 +1,395 @@
+// LayerNorm(x + residual) over rows of `cols` elements and its gradient: the
+// layer's closing step (aifetchly-blog.pages.dev, "Gated DeltaNet-2 Guide",
+// "End-to-End PyTorch Implementation": LayerNorm(x + out_proj(y))).
+//
+//   h = x + residual,  mean = sum h / n,  var = sum (h - mean)^2 / n,
+//   rstd = 1 / sqrt(var + eps),  y = (h - mean) rstd weight + bias
+//
+//   backward, with xh = (h - mean) rstd and g = dy weight:
+//   dh = rstd (g - sum(g) / n - xh sum(g xh) / n) [+ dsum]
+//   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+//
+// A row is read once and held in registers by TPR threads (a part of a wave,
+// a wave or a workgroup), E packs of V elements each; mean and variance are
+// two passes over the registers, so an offset far from zero costs no
+// precision. Everything is fp32; y, sum and dh are rounded once, as they are
+// stored. The statistics are those of the unrounded sum. Rows too long for
+// the registers are read again for each pass (they stay in the L2).
+//
+// The backward takes the sum h and forms its statistics anew: the row is in
+// registers anyway, and its gradient is then that of the h it was given.
+// Each workgroup adds its rows' terms of dweight and dbias in registers, in
+// row order, and writes one partial row; a second kernel adds the partial
+// rows in a fixed order (no atomics: the same inputs give the same bits).
+#include "gdn2_launch.hpp"
+#include "rows.hpp"
+
+#include <algorithm>
+
+namespace gdn2 {
+
+template <int TPR> struct RowShape {
+    static constexpr int NT = TPR > 256 ? TPR : 256;   // threads
+    static constexpr int RPB = NT / TPR;               // rows of a workgroup
+};
+
+template <typename In, typename Out, int V, int TPR, int E, bool RES>
+__global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_fwd_kernel(
+    const In *x, const In *res, const float *__restrict__ weight, const float *__restrict__ bias, Out *y, In *sum,
+    int64_t rows, int cols, float inv_n, float eps)
+{
+    constexpr int RPB = RowShape<TPR>::RPB;
+    __shared__ float red[TPR > 64 ? TPR / 64 : 1];
+    const int p = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    float wv[E][V], bv[E][V];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = (p + e * TPR) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            wv[e][i] = c < cols ? weight[c + i] : 0.f;
+            bv[e][i] = c < cols && bias ? bias[c + i] : 0.f;
+        }
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
+        // groups past the last row repeat it and store nothing
+        const bool live = r0 + grp < rows;
+        const int64_t base = (live ? r0 + grp : rows - 1) * (int64_t)cols;
+        Pack<In, V> px[E], pr[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = (p + e * TPR) * V;
+            px[e].zero();
+            if (RES) pr[e].zero();
+            if (c < cols) {
+                px[e].load(x + base + c);
+                if (RES) pr[e].load(res + base + c);
+            }
+        }
+        float h[E][V], s[1] = {0.f};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                h[e][i] = RES ? px[e].get(i) + pr[e].get(i) : px[e].get(i);
+                s[0] += h[e][i];
+            }
+        row_sums<TPR>(s, red);
+        const float mean = s[0] * inv_n;
+        s[0] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if ((p + e * TPR) * V < cols)
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[0] += (h[e][i] - mean) * (h[e][i] - mean);
+        row_sums<TPR>(s, red);
+        const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
+        if (live)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int c = (p + e * TPR) * V;
+                if (c < cols) {
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[i] = (h[e][i] - mean) * rstd * wv[e][i] + bv[e][i];
+                    store_row<V>(y + base + c, o);
+                    if (sum) store_row<V>(sum + base + c, h[e]);
+                }
+            }
+    }
+}
+
+// Rows longer than the registers hold: one workgroup a row, three passes.
+template <typename In, typename Out>
+__global__ __launch_bounds__(1024) void ln_fwd_long_kernel(
+    const In *x, const In *res, const float *__restrict__ weight, const float *__restrict__ bias, Out *y, In *sum,
+    int64_t rows, int cols, float inv_n, float eps)
+{
+    __shared__ float red[16];
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int64_t base = r * (int64_t)cols;
+        auto at = [&](int c) { return in2f<In>(x[base + c]) + (res ? in2f<In>(res[base + c]) : 0.f); };
+        float s[1] = {0.f};
+        for (int c = threadIdx.x; c < cols; c += 1024) s[0] += at(c);
+        row_sums<1024>(s, red);
+        const float mean = s[0] * inv_n;
+        s[0] = 0.f;
+        for (int c = threadIdx.x; c < cols; c += 1024) s[0] += (at(c) - mean) * (at(c) - mean);
+        row_sums<1024>(s, red);
+        const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
+        for (int c = threadIdx.x; c < cols; c += 1024) {
+            const float h = at(c), o = (h - mean) * rstd * weight[c] + (bias ? bias[c] : 0.f);
+            store_row<1>(y + base + c, &o);
+            if (sum) store_row<1>(sum + base + c, &h);
+        }
+    }
+}
+
+// Gradient. part: [gridDim.x][2][cols], this workgroup's sums of dy xh and dy.
+template <typename In, typename Dy, int V, int TPR, int E>
+__global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_bwd_kernel(
+    const Dy *dy, const In *h, const float *__restrict__ weight, const In *dsum, In *dh, float *__restrict__ part,
+    int64_t rows, int cols, float inv_n, float eps)
+{
+    constexpr int RPB = RowShape<TPR>::RPB;
+    __shared__ float red[TPR > 64 ? 2 * (TPR / 64) : 1];
+    const int p = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    float wv[E][V], dw[E][V], db[E][V];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = (p + e * TPR) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            wv[e][i] = c < cols ? weight[c + i] : 0.f;
+            dw[e][i] = db[e][i] = 0.f;
+        }
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
+        const bool live = r0 + grp < rows;
+        const int64_t base = (live ? r0 + grp : rows - 1) * (int64_t)cols;
+        Pack<In, V> ph[E], pa[E];
+        Pack<Dy, V> pd[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = (p + e * TPR) * V;
+            ph[e].zero();
+            pd[e].zero();
+            pa[e].zero();
+            if (c < cols) {
+                ph[e].load(h + base + c);
+                pd[e].load(dy + base + c);
+                if (dsum) pa[e].load(dsum + base + c);
+            }
+        }
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[0] += ph[e].get(i);
+                s[1] += pd[e].get(i) * wv[e][i];
+            }
+        row_sums<TPR>(s, red);
+        const float mean = s[0] * inv_n, gm = s[1] * inv_n;
+        s[0] = s[1] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if ((p + e * TPR) * V < cols)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float c = ph[e].get(i) - mean;
+                    s[0] += c * c;
+                    s[1] += c * (pd[e].get(i) * wv[e][i]);
+                }
+        row_sums<TPR>(s, red);
+        const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
+        const float gx = s[1] * rstd * inv_n;   // mean of g xh
+        if (live)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int c = (p + e * TPR) * V;
+                if (c < cols) {
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float xh = (ph[e].get(i) - mean) * rstd, d = pd[e].get(i);
+                        o[i] = rstd * (d * wv[e][i] - gm - xh * gx);
+                        if (dsum) o[i] += pa[e].get(i);
+                        dw[e][i] += d * xh;
+                        db[e][i] += d;
+                    }
+                    store_row<V>(dh + base + c, o);
+                }
+            }
+    }
+    // the groups' sums, in group order, to this workgroup's partial row
+    float *pw = part + (size_t)blockIdx.x * 2 * cols;
+    if constexpr (RPB == 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = (p + e * TPR) * V;
+            if (c < cols) {
+                store_row<V>(pw + c, dw[e]);
+                store_row<V>(pw + cols + c, db[e]);
+            }
+        }
+    } else {
+        __shared__ float acc[RPB][TPR * V];
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[grp][p * V + i] = e < E ? dw[e % E][i] : db[e % E][i];
+            __syncthreads();
+            for (int c = threadIdx.x; c < TPR * V; c += RowShape<TPR>::NT) {
+                const int cc = (e % E) * TPR * V + c;
+                if (cc < cols) {
+                    float t = 0.f;
+#pragma unroll
+                    for (int g = 0; g < RPB; ++g) t += acc[g][c];
+                    pw[(e < E ? 0 : cols) + cc] = t;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Long rows: one workgroup a row at a time; its partial row is added to in
+// place (the same thread owns a column throughout).
+template <typename In, typename Dy>
+__global__ __launch_bounds__(1024) void ln_bwd_long_kernel(
+    const Dy *dy, const In *h, const float *__restrict__ weight, const In *dsum, In *dh, float *part, int64_t rows,
+    int cols, float inv_n, float eps)
+{
+    __shared__ float red[32];
+    float *pw = part + (size_t)blockIdx.x * 2 * cols;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int64_t base = r * (int64_t)cols;
+        float s[2] = {0.f, 0.f};
+        for (int c = threadIdx.x; c < cols; c += 1024) {
+            s[0] += in2f<In>(h[base + c]);
+            s[1] += in2f<Dy>(dy[base + c]) * weight[c];
+        }
+        row_sums<1024>(s, red);
+        const float mean = s[0] * inv_n, gm = s[1] * inv_n;
+        s[0] = s[1] = 0.f;
+        for (int c = threadIdx.x; c < cols; c += 1024) {
+            const float x = in2f<In>(h[base + c]) - mean;
+            s[0] += x * x;
+            s[1] += x * (in2f<Dy>(dy[base + c]) * weight[c]);
+        }
+        row_sums<1024>(s, red);
+        const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
+        const float gx = s[1] * rstd * inv_n;
+        const bool first = r == blockIdx.x;
+        for (int c = threadIdx.x; c < cols; c += 1024) {
+            const float xh = (in2f<In>(h[base + c]) - mean) * rstd, d = in2f<Dy>(dy[base + c]);
+            float o = rstd * (d * weight[c] - gm - xh * gx);
+            if (dsum) o += in2f<In>(dsum[base + c]);
+            store_row<1>(dh + base + c, &o);
+            pw[c] = (first ? 0.f : pw[c]) + d * xh;
+            pw[cols + c] = (first ? 0.f : pw[cols + c]) + d;
+        }
+    }
+}
+
+// ---- launch ------------------------------------------------------------------
+
+// Calls f with the (V, TPR, E) that holds a row of `cols` elements in
+// registers, or returns false (the long-row kernels take it). V = 8 where
+// rows keep 16-byte alignment (cols a multiple of 8).
+template <typename F> static bool for_row_shape(int cols, F f)
+{
+    auto go = [&](auto v, auto t, auto e) {
+        f(v, t, e);
+        return true;
+    };
+#define GDN2_ROW(V, T, E) \
+    if (cols <= V * T * E) \
+        return go(std::integral_constant<int, V>{}, std::integral_constant<int, T>{}, std::integral_constant<int, E>{});
+    if (cols % 8 == 0) {
+        GDN2_ROW(8, 8, 1)
+        GDN2_ROW(8, 16, 1)
+        GDN2_ROW(8, 32, 1)
+        GDN2_ROW(8, 64, 1)
+        GDN2_ROW(8, 64, 2)
+        GDN2_ROW(8, 64, 4)
+        GDN2_ROW(8, 256, 2)
+        GDN2_ROW(8, 256, 4)
+        GDN2_ROW(8, 1024, 2)
+    } else {
+        GDN2_ROW(1, 8, 1)
+        GDN2_ROW(1, 16, 1)
+        GDN2_ROW(1, 64, 1)
+        GDN2_ROW(1, 64, 4)
+        GDN2_ROW(1, 256, 4)
+        GDN2_ROW(1, 256, 16)
+        GDN2_ROW(1, 1024, 16)
+    }
+#undef GDN2_ROW
+    return false;
+}
+
+static int ln_grid(int64_t rows, int rpb, int most) { return (int)std::min<int64_t>((rows + rpb - 1) / rpb, most); }
+
+template <typename In, typename Out> static void ln_fwd(const LayerNormArgs &a, hipStream_t st)
+{
+    const float inv_n = 1.f / (float)a.cols;
+    auto args = [&](auto kern, int grid, int nt) {
+        hipLaunchKernelGGL(kern, dim3(grid), dim3(nt), 0, st, (const In *)a.x, (const In *)a.residual, a.weight, a.bias,
+                           (Out *)a.y, (In *)a.sum, a.rows, a.cols, inv_n, a.eps);
+    };
+    const bool held = for_row_shape(a.cols, [&](auto v, auto t, auto e) {
+        constexpr int V = decltype(v)::value, T = decltype(t)::value, E = decltype(e)::value;
+        const int grid = ln_grid(a.rows, RowShape<T>::RPB, kLnFwdGrid);
+        if (a.residual) args(ln_fwd_kernel<In, Out, V, T, E, true>, grid, RowShape<T>::NT);
+        else args(ln_fwd_kernel<In, Out, V, T, E, false>, grid, RowShape<T>::NT);
+    });
+    if (!held) args(ln_fwd_long_kernel<In, Out>, ln_grid(a.rows, 1, kLnFwdGrid), 1024);
+}
+
+template <typename In, typename Dy> static void ln_bwd(const LayerNormBwdArgs &a, hipStream_t st)
+{
+    const float inv_n = 1.f / (float)a.cols;
+    auto args = [&](auto kern, int grid, int nt) {
+        hipLaunchKernelGGL(kern, dim3(grid), dim3(nt), 0, st, (const Dy *)a.dy, (const In *)a.h, a.weight,
+                           (const In *)a.dsum, (In *)a.dh, (float *)a.workspace, a.rows, a.cols, inv_n, a.eps);
+    };
+    const int grid = ln_bwd_parts(a.rows, a.cols);
+    const bool held = for_row_shape(a.cols, [&](auto v, auto t, auto e) {
+        constexpr int V = decltype(v)::value, T = decltype(t)::value, E = decltype(e)::value;
+        args(ln_bwd_kernel<In, Dy, V, T, E>, grid, RowShape<T>::NT);
+    });
+    if (!held) args(ln_bwd_long_kernel<In, Dy>, grid, 1024);
+}
+
+int ln_bwd_parts(int64_t rows, int cols)
+{
+    int rpb = 1;
+    (void)for_row_shape(cols, [&](auto, auto t, auto) { rpb = RowShape<decltype(t)::value>::RPB; });
+    // (wide rows: fewer parts, so that the partial rows stay within 64 MiB, or 32 rows)
+    return ln_grid(rows, rpb, std::max(32, std::min(kLnBwdGrid, (1 << 23) / cols)));
+}
+
+hipError_t launch_layer_norm_fwd(const LayerNormArgs &a, hipStream_t st)
+{
+    if (a.rows == 0) return hipSuccess;
+    prof_before("gdn2_layer_norm_fwd", st);
+    if (a.in_bf16) {
+        if (a.out_bf16) ln_fwd<uint16_t, uint16_t>(a, st);
+        else ln_fwd<uint16_t, float>(a, st);
+    } else {
+        if (a.out_bf16) ln_fwd<float, uint16_t>(a, st);
+        else ln_fwd<float, float>(a, st);
+    }
+    prof_after(st);
+    return hipGetLastError();
+}
+
+hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs &a, hipStream_t st)
+{
+    if (a.rows > 0) {
+        prof_before("gdn2_layer_norm_bwd", st);
+        if (a.in_bf16) {
+            if (a.out_bf16) ln_bwd<uint16_t, uint16_t>(a, st);
+            else ln_bwd<uint16_t, float>(a, st);
+        } else {
+            if (a.out_bf16) ln_bwd<float, uint16_t>(a, st);
+            else ln_bwd<float, float>(a, st);
+        }
+        prof_after(st);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    // (no rows: no parts, and the weights' gradients are zeros)
+    ColumnSums c = {};
+    c.part[0] = (const float *)a.workspace;
+    c.out0[0] = a.dweight;
+    c.out1[0] = a.dbias;
+    c.n0[0] = c.n1[0] = a.cols;
+    c.parts = ln_bwd_parts(a.rows, a.cols);
+    c.jobs = 1;
+    return launch_column_sums(c, "gdn2_layer_norm_reduce", st);
+}
+
+} // namespace gdn2

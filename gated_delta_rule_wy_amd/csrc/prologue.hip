@@ -1,0 +1,602 @@
+// The input prologue on its own and its gradient: short causal depthwise
+// convolution of 4 taps on q, k, v, unit norm of q and k over a head's
+// channels, sigmoid of the gate logits (aifetchly-blog.pages.dev, "Gated
+// DeltaNet-2 Guide", the "Architectural Workflow" diagram, steps 1 and 2).
+//
+//   y_t = bias + sum_j w_j x_{t-3+j},   q = y r,  r = 1 / max(|y|, 1e-12)
+//   gate = 1 / (1 + exp(-logit))
+//   backward: dy = dq (v), dy = r dq - y r^3 (y.dq) (q, k; r dq where |y| <= 1e-12)
+//     dx_t = sum_j w_j dy_{t+3-j},  dw_j = sum_t dy_t x_{t-3+j},  dbias = sum_t dy_t
+//     dlogit = dgate s (1 - s)
+//
+// Bound by memory: every element is read once and written once. A thread owns
+// V neighbouring channels of one tensor (16 bytes of bf16; the lanes of a head
+// are neighbours, and its norm a sum over them) and walks along the tokens
+// with the last three inputs in registers, four rows of loads ahead. All sums
+// are fp32; outputs are rounded once.
+#include "gdn2_launch.hpp"
+#include "rows.hpp"
+
+#include <algorithm>
+
+namespace gdn2 {
+
+constexpr int kNT = 256;
+
+// Sum over aligned groups of G lanes, G a power of two up to 32, in each of
+// them; the group's lanes are active together.
+__device__ __forceinline__ float head_sum(float x, int G)
+{
+    if (G >= 2) x += __shfl_xor(x, 1);
+    if (G >= 4) x += __shfl_xor(x, 2);
+    if (G >= 8) x += __shfl_xor(x, 4);
+    if (G >= 16) x += __shfl_xor(x, 8);
+    if (G >= 32) x += __shfl_xor(x, 16);
+    return x;
+}
+
+struct SeqTable {
+    const int32_t *cu;   // or null: sequences of T tokens
+    int T, N;            // T: tokens of a sequence, or in all
+    __device__ __forceinline__ int total() const { return cu ? min(max(cu[N], 0), T) : N * T; }
+    // (bounds of a table that is not what it has to be still lie within [0, T])
+    __device__ __forceinline__ int start(int i) const { return cu ? (i > 0 ? min(max(cu[i], 0), T) : 0) : i * T; }
+    __device__ __forceinline__ int end(int i) const { return cu ? min(max(cu[i + 1], start(i)), T) : (i + 1) * T; }
+    // the first sequence behind i that ends behind token t
+    __device__ __forceinline__ int next(int i, int t) const
+    {
+        while (i < N - 1)
+            if (end(++i) > t) break;
+        return i;
+    }
+    // the last sequence that starts at or before token t
+    __device__ __forceinline__ int of(int t) const
+    {
+        if (!cu) return min(t / T, N - 1);
+        int lo = 0, hi = N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cu[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+// V channels of one tensor and token, packed.
+template <typename In, int V> struct PackV {
+    In e[V] __attribute__((aligned(V * sizeof(In) > 16 ? 16 : V * sizeof(In))));
+    __device__ __forceinline__ void load(const In *p)
+    {
+        constexpr int B = V * sizeof(In);
+        if constexpr (B == 8) *reinterpret_cast<uint2 *>(e) = *reinterpret_cast<const uint2 *>(p);
+        else
+#pragma unroll
+            for (int i = 0; i < B / 16; ++i) reinterpret_cast<u4 *>(e)[i] = reinterpret_cast<const u4 *>(p)[i];
+    }
+    __device__ __forceinline__ void store(In *p) const
+    {
+        constexpr int B = V * sizeof(In);
+        if constexpr (B == 8) *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(e);
+        else
+#pragma unroll
+            for (int i = 0; i < B / 16; ++i) reinterpret_cast<u4 *>(p)[i] = reinterpret_cast<const u4 *>(e)[i];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = (In)0;
+    }
+    __device__ __forceinline__ float get(int i) const { return in2f<In>(e[i]); }
+};
+template <typename T> __device__ __forceinline__ T from_f(float x)
+{
+    if constexpr (sizeof(T) == 4) return x;
+    else return (uint16_t)bf16x2(x, 0.f);
+}
+
+// One tensor's part of a launch.
+struct ProTensor {
+    const void *x;
+    const float *w, *bias;
+    const void *hin;
+    void *hout;
+    void *y;
+    int heads, d;        // channels a token: heads * d
+    int block0, blocks;  // its workgroups
+};
+struct ProGate {
+    const void *x;
+    void *y;
+    const float *dy;
+    int n;               // values a token
+    int block0, blocks;
+};
+struct ProParams {
+    ProTensor t[3];
+    ProGate g[2];
+    SeqTable sq;
+    const int32_t *slot_in, *slot_out, *commit;
+    int slots, tile;     // tokens a thread walks over
+};
+
+// History element j (0..2, oldest first) of sequence i for the V channels at
+// ch (head ch / d), or zeros.
+template <typename In, int V>
+__device__ __forceinline__ void load_history(PackV<In, V> &r, const ProTensor &t, const ProParams &p, int i, int j, int ch)
+{
+    const int slot = p.slot_in ? p.slot_in[i] : i;
+    if (t.hin && (unsigned)slot < (unsigned)p.slots)
+        r.load((const In *)t.hin + (((size_t)slot * t.heads + ch / t.d) * 3 + j) * t.d + ch % t.d);
+    else r.zero();
+}
+
+// x rows p0 + 0 .. 2 (positions in the sequence, negative ones from the
+// history) into win[0..2].
+template <typename In, int V>
+__device__ __forceinline__ void load_window(PackV<In, V> (&win)[3], const ProTensor &t, const ProParams &p, int i, int s0,
+                                            int pos, int ch)
+{
+    const size_t W = (size_t)t.heads * t.d;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const int q = pos + j;
+        if (q >= 0) win[j].load((const In *)t.x + (size_t)(s0 + q) * W + ch);
+        else load_history<In, V>(win[j], t, p, i, 3 + q, ch);
+    }
+}
+
+// ---- forward -------------------------------------------------------------------
+
+template <typename In>
+__device__ void gate_fwd(const ProGate &gt, int64_t total, int block)
+{
+    const int64_t n = total * gt.n, at = ((int64_t)block * kNT + threadIdx.x) * 8;
+    if (at >= n) return;
+    const In *x = (const In *)gt.x + at;
+    In *y = (In *)gt.y + at;
+    auto one = [](float z) { return from_f<In>(__builtin_amdgcn_rcpf(1.f + __expf(-z))); };
+    if (at + 8 <= n) {
+        PackV<In, 8> r;
+        r.load(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.e[i] = one(r.get(i));
+        r.store(y);
+    } else {
+        for (int i = 0; i < (int)(n - at); ++i) y[i] = one(in2f<In>(x[i]));
+    }
+}
+
+// OWN: the thread's tile is one whole sequence (short ones), and it also
+// writes the sequence's new history, after reading the old one.
+template <typename In, bool OWN>
+__global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
+{
+    constexpr int V = 8, U = 4;
+    const int total = p.sq.total();
+    const int bid = blockIdx.x;
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+        if (bid >= p.g[z].block0 && bid < p.g[z].block0 + p.g[z].blocks) {
+            gate_fwd<In>(p.g[z], total, bid - p.g[z].block0);
+            return;
+        }
+    const int z = bid >= p.t[2].block0 ? 2 : (bid >= p.t[1].block0 ? 1 : 0);
+    const ProTensor &t = p.t[z];
+    const size_t W = (size_t)t.heads * t.d;
+    const int nvec = (int)(W / V), G = t.d / V;
+    const int64_t id = (int64_t)(bid - t.block0) * kNT + threadIdx.x;
+    const int64_t tl = id / nvec;
+    const int ch = (int)(id % nvec) * V;
+    int i, tb, te;
+    if (OWN) {
+        if (tl >= p.sq.N) return;   // (a head's lanes leave together)
+        i = (int)tl;
+        tb = p.sq.start(i);
+        te = p.sq.end(i);
+    } else {
+        if (tl * p.tile >= total) return;
+        tb = (int)(tl * p.tile);
+        te = min(tb + p.tile, total);
+        i = p.sq.of(tb);
+    }
+    const In *x = (const In *)t.x;
+    In *y = (In *)t.y;
+    f4 tap[V];
+    float bias[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        tap[c] = *reinterpret_cast<const f4 *>(t.w + 4 * (size_t)(ch + c));
+        bias[c] = t.bias ? t.bias[ch + c] : 0.f;
+    }
+    PackV<In, V> win[3];
+    int s0 = p.sq.start(i), s1 = p.sq.end(i);
+    load_window<In, V>(win, t, p, i, s0, tb - s0 - 3, ch);
+    PackV<In, V> nxt[U];
+    if (tb < te)
+#pragma unroll
+        for (int u = 0; u < U; ++u) nxt[u].load(x + (size_t)min(tb + u, te - 1) * W + ch);
+    for (int tok = tb; tok < te; tok += U) {
+        PackV<In, V> cur[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) cur[u] = nxt[u];
+#pragma unroll
+        for (int u = 0; u < U; ++u) nxt[u].load(x + (size_t)min(tok + U + u, te - 1) * W + ch);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = tok + u;
+            if (at < te) {
+                if (!OWN && at >= s1) {   // the next sequence with tokens
+                    i = p.sq.next(i, at);
+                    s0 = p.sq.start(i);
+                    s1 = p.sq.end(i);
+                    load_window<In, V>(win, t, p, i, s0, -3, ch);
+                }
+                float o[V], ss = 0.f;
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    o[c] = bias[c] + tap[c][0] * win[0].get(c) + tap[c][1] * win[1].get(c) + tap[c][2] * win[2].get(c) +
+                           tap[c][3] * cur[u].get(c);
+                    ss += o[c] * o[c];
+                }
+                if (z < 2) {
+                    const float r = rsqrtf(fmaxf(head_sum(ss, G), 1e-24f));
+#pragma unroll
+                    for (int c = 0; c < V; ++c) o[c] *= r;
+                }
+                store_row<V>(y + (size_t)at * W + ch, o);
+                win[0] = win[1];
+                win[1] = win[2];
+                win[2] = cur[u];
+            }
+        }
+    }
+    if (OWN && t.hout) {
+        const int slot = p.slot_out ? p.slot_out[i] : (p.slot_in ? p.slot_in[i] : i);
+        if ((unsigned)slot >= (unsigned)p.slots) return;
+        const int keep = p.commit ? min(max(p.commit[i], 0), te - tb) : te - tb;
+        PackV<In, V> h[3];
+        load_window<In, V>(h, t, p, i, tb, keep - 3, ch);
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            h[j].store((In *)t.hout + (((size_t)slot * t.heads + ch / t.d) * 3 + j) * t.d + ch % t.d);
+    }
+}
+
+// New histories of sequences that several threads walked over. A thread owns
+// V channels of one sequence's three rows and reads them all before it writes.
+template <typename In> __global__ __launch_bounds__(kNT) void prologue_history_kernel(ProParams p)
+{
+    constexpr int V = 8;
+    const ProTensor &t = p.t[blockIdx.y];
+    const int nvec = t.heads * t.d / V;
+    const int64_t id = (int64_t)blockIdx.x * kNT + threadIdx.x;
+    const int64_t tl = id / nvec;
+    if (tl >= p.sq.N) return;
+    const int i = (int)tl, ch = (int)(id % nvec) * V;
+    const int slot = p.slot_out ? p.slot_out[i] : (p.slot_in ? p.slot_in[i] : i);
+    if ((unsigned)slot >= (unsigned)p.slots) return;
+    const int tb = p.sq.start(i), len = p.sq.end(i) - tb;
+    const int keep = p.commit ? min(max(p.commit[i], 0), len) : len;
+    PackV<In, V> h[3];
+    load_window<In, V>(h, t, p, i, tb, keep - 3, ch);
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+        h[j].store((In *)t.hout + (((size_t)slot * t.heads + ch / t.d) * 3 + j) * t.d + ch % t.d);
+}
+
+// ---- backward ------------------------------------------------------------------
+
+struct ProBwdParams {
+    ProParams f;
+    const float *dy[3];
+    void *dx[3];
+    float *part[3];      // [tiles][5 * channels]: 4 tap sums a channel, then the bias sums
+};
+
+template <typename In, typename Out>
+__device__ void gate_bwd(const ProGate &gt, int64_t total, int block)
+{
+    const int64_t n = total * gt.n, at = ((int64_t)block * kNT + threadIdx.x) * 8;
+    if (at >= n) return;
+    const In *x = (const In *)gt.x + at;
+    const float *dy = gt.dy + at;
+    Out *dx = (Out *)gt.y + at;
+    auto one = [](float z, float d) {
+        const float s = __builtin_amdgcn_rcpf(1.f + __expf(-z));
+        return d * s * (1.f - s);
+    };
+    if (at + 8 <= n) {
+        PackV<In, 8> r;
+        PackV<float, 8> d;
+        r.load(x);
+        d.load(dy);
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = one(r.get(i), d.e[i]);
+        store_row<8>(dx, o);
+    } else {
+        for (int i = 0; i < (int)(n - at); ++i) dx[i] = from_f<Out>(one(in2f<In>(x[i]), dy[i]));
+    }
+}
+
+template <typename In, typename Out>
+__global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
+{
+    constexpr int V = 4, U = 4;
+    const int total = p.f.sq.total();
+    const int bid = blockIdx.x;
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+        if (bid >= p.f.g[z].block0 && bid < p.f.g[z].block0 + p.f.g[z].blocks) {
+            gate_bwd<In, Out>(p.f.g[z], total, bid - p.f.g[z].block0);
+            return;
+        }
+    const int z = bid >= p.f.t[2].block0 ? 2 : (bid >= p.f.t[1].block0 ? 1 : 0);
+    const ProTensor &t = p.f.t[z];
+    const size_t W = (size_t)t.heads * t.d;
+    const int nvec = (int)(W / V), G = t.d / V;
+    const int64_t id = (int64_t)(bid - t.block0) * kNT + threadIdx.x;
+    const int64_t tl = id / nvec;
+    const int ch = (int)(id % nvec) * V;
+    // every tile up to the last token the sizes allow has its partial row;
+    // those behind the last sequence write zeros
+    if (tl * p.f.tile >= (p.f.sq.cu ? (int64_t)p.f.sq.T : (int64_t)p.f.sq.N * p.f.sq.T)) return;
+    f4 dw[V];
+    float db[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        dw[c] = f4zero();
+        db[c] = 0.f;
+    }
+    if (tl * p.f.tile < total) {
+        const int tb = (int)(tl * p.f.tile), te = min(tb + p.f.tile, total);
+        const In *x = (const In *)t.x;
+        const float *dy = p.dy[z];
+        Out *dx = (Out *)p.dx[z];
+        f4 tap[V];
+        float bias[V], a[3][V];   // a[j]: what is known of dx of the token j + 1 back
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            tap[c] = *reinterpret_cast<const f4 *>(t.w + 4 * (size_t)(ch + c));
+            bias[c] = t.bias ? t.bias[ch + c] : 0.f;
+            a[0][c] = a[1][c] = a[2][c] = 0.f;
+        }
+        int i = p.f.sq.of(tb), s0 = p.f.sq.start(i), s1 = p.f.sq.end(i);
+        PackV<In, V> win[3];
+        load_window<In, V>(win, t, p.f, i, s0, tb - s0 - 3, ch);
+        // up to three tokens past the tile, of the sequence of its last one
+        const int il = p.f.sq.of(te - 1);
+        const int th = max(te, min(te + 3, p.f.sq.end(il)));
+        PackV<In, V> nx[U];
+        PackV<float, V> nd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            nx[u].load(x + (size_t)min(tb + u, th - 1) * W + ch);
+            nd[u].load(dy + (size_t)min(tb + u, th - 1) * W + ch);
+        }
+        for (int tok = tb; tok < th; tok += U) {
+            PackV<In, V> cx[U];
+            PackV<float, V> cd[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                cx[u] = nx[u];
+                cd[u] = nd[u];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                nx[u].load(x + (size_t)min(tok + U + u, th - 1) * W + ch);
+                nd[u].load(dy + (size_t)min(tok + U + u, th - 1) * W + ch);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = tok + u;
+                if (at < th) {
+                    if (at >= s1) {
+                        i = p.f.sq.next(i, at);
+                        s0 = p.f.sq.start(i);
+                        s1 = p.f.sq.end(i);
+                        load_window<In, V>(win, t, p.f, i, s0, -3, ch);
+                    }
+                    float d[V];
+#pragma unroll
+                    for (int c = 0; c < V; ++c) d[c] = cd[u].e[c];
+                    if (z < 2) {
+                        float y[V], ss = 0.f, yd = 0.f;
+#pragma unroll
+                        for (int c = 0; c < V; ++c) {
+                            y[c] = bias[c] + tap[c][0] * win[0].get(c) + tap[c][1] * win[1].get(c) +
+                                   tap[c][2] * win[2].get(c) + tap[c][3] * cx[u].get(c);
+                            ss += y[c] * y[c];
+                            yd += y[c] * d[c];
+                        }
+                        ss = head_sum(ss, G);
+                        yd = head_sum(yd, G);
+                        const float r = rsqrtf(fmaxf(ss, 1e-24f));
+                        // (r y).dq along the unit vector; none where the norm is at its floor
+                        const float m = ss > 1e-24f ? r * yd * r : 0.f;
+#pragma unroll
+                        for (int c = 0; c < V; ++c) d[c] = r * (d[c] - m * y[c]);
+                    }
+                    if (at < te) {
+#pragma unroll
+                        for (int c = 0; c < V; ++c) {
+                            dw[c][0] += d[c] * win[0].get(c);
+                            dw[c][1] += d[c] * win[1].get(c);
+                            dw[c][2] += d[c] * win[2].get(c);
+                            dw[c][3] += d[c] * cx[u].get(c);
+                            db[c] += d[c];
+                        }
+                    }
+                    // dx of the token three back is complete; the others move up
+                    float o[V];
+#pragma unroll
+                    for (int c = 0; c < V; ++c) {
+                        o[c] = a[2][c] + tap[c][0] * d[c];
+                        a[2][c] = a[1][c] + tap[c][1] * d[c];
+                        a[1][c] = a[0][c] + tap[c][2] * d[c];
+                        a[0][c] = tap[c][3] * d[c];
+                    }
+                    const int low = max(tb, s0);
+                    auto put = [&](int to, const float *v) {
+                        if (to >= low && to < te) store_row4(dx + (size_t)to * W + ch, v);
+                    };
+                    put(at - 3, o);
+                    if (at == s1 - 1) {   // the sequence's last token: nothing follows
+                        put(at - 2, a[2]);
+                        put(at - 1, a[1]);
+                        put(at, a[0]);
+#pragma unroll
+                        for (int c = 0; c < V; ++c) a[0][c] = a[1][c] = a[2][c] = 0.f;
+                    }
+                    win[0] = win[1];
+                    win[1] = win[2];
+                    win[2] = cx[u];
+                }
+            }
+        }
+    }
+    float *part = p.part[z] + (size_t)tl * 5 * W;
+#pragma unroll
+    for (int c = 0; c < V; ++c) *reinterpret_cast<f4 *>(part + 4 * (size_t)(ch + c)) = dw[c];
+    f4 b4 = {db[0], db[1], db[2], db[3]};
+    *reinterpret_cast<f4 *>(part + 4 * W + ch) = b4;
+}
+
+// ---- launch --------------------------------------------------------------------
+
+static int64_t tokens_of(const PrologueArgs &a) { return a.cu_seqlens ? (int64_t)a.T : (int64_t)a.N * a.T; }
+
+static ProParams pro_params(const PrologueArgs &a, int V, int64_t tiles, int tile, int *blocks)
+{
+    ProParams p = {};
+    int at = 0;
+    for (int z = 0; z < 3; ++z) {
+        ProTensor &t = p.t[z];
+        t.x = a.x[z];
+        t.w = a.weight[z];
+        t.bias = a.bias[z];
+        t.hin = a.hist_in[z];
+        t.hout = a.hist_out[z];
+        t.y = a.y[z];
+        t.heads = a.heads[z];
+        t.d = a.d[z];
+        t.block0 = at;
+        t.blocks = (int)((tiles * (t.heads * t.d / V) + kNT - 1) / kNT);
+        at += t.blocks;
+    }
+    for (int z = 0; z < 2; ++z) {
+        ProGate &g = p.g[z];
+        g.x = a.logit[z];
+        g.y = a.gate[z];
+        g.n = a.nlogit[z];
+        g.block0 = at;
+        g.blocks = (int)((tokens_of(a) * g.n + 8 * kNT - 1) / (8 * kNT));
+        at += g.blocks;
+    }
+    p.sq = {a.cu_seqlens, a.T, a.N};
+    p.slot_in = a.slot_in;
+    p.slot_out = a.slot_out;
+    p.commit = a.commit;
+    p.slots = a.slots;
+    p.tile = tile;
+    *blocks = at;
+    return p;
+}
+
+// Sequences of at most this many tokens are walked by one thread a channel
+// group each, which then also writes their histories (one launch).
+constexpr int kOwnTokens = 16;
+
+template <typename In> static hipError_t prologue_fwd_t(const PrologueArgs &a, hipStream_t st)
+{
+    const bool own = a.T <= kOwnTokens, hist = a.hist_out[0] != nullptr;
+    const int64_t tokens = tokens_of(a);
+    const int tile = 32;
+    int blocks = 0;
+    const ProParams p = pro_params(a, 8, own ? a.N : (tokens + tile - 1) / tile, tile, &blocks);
+    if (blocks > 0 && (tokens > 0 || (own && hist))) {
+        prof_before("gdn2_prologue_fwd", st);
+        if (own) hipLaunchKernelGGL((prologue_fwd_kernel<In, true>), dim3(blocks), dim3(kNT), 0, st, p);
+        else hipLaunchKernelGGL((prologue_fwd_kernel<In, false>), dim3(blocks), dim3(kNT), 0, st, p);
+        prof_after(st);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    if (own || !hist) return hipSuccess;
+    int widest = 0;
+    for (int z = 0; z < 3; ++z) widest = std::max(widest, a.heads[z] * a.d[z]);
+    prof_before("gdn2_prologue_history", st);
+    hipLaunchKernelGGL((prologue_history_kernel<In>), dim3((unsigned)(((int64_t)a.N * (widest / 8) + kNT - 1) / kNT), 3),
+                       dim3(kNT), 0, st, p);
+    prof_after(st);
+    return hipGetLastError();
+}
+
+hipError_t launch_prologue_fwd(const PrologueArgs &a, hipStream_t st)
+{
+    return a.bf16 ? prologue_fwd_t<uint16_t>(a, st) : prologue_fwd_t<float>(a, st);
+}
+
+// Tokens a backward thread walks over (four channels each): enough threads to
+// fill the chip twice over (256 CUs x 8 waves), between 16 and 256 tokens (a
+// tile reads three rows before and three after its own).
+int prologue_bwd_tile(long long tokens, long long channels)
+{
+    const long long t = tokens * (channels / 4) / (256LL * 8 * 64);
+    return (int)std::max(16LL, std::min(256LL, (t + 3) / 4 * 4));
+}
+
+size_t prologue_bwd_workspace(long long tokens, long long channels)
+{
+    const long long tile = prologue_bwd_tile(tokens, channels);
+    return (size_t)((tokens + tile - 1) / tile) * 5 * channels * sizeof(float);
+}
+
+template <typename In, typename Out> static hipError_t prologue_bwd_t(const PrologueBwdArgs &a, hipStream_t st)
+{
+    const int64_t tokens = tokens_of(a.f);
+    int64_t channels = 0;
+    for (int z = 0; z < 3; ++z) channels += a.f.heads[z] * a.f.d[z];
+    const int tile = prologue_bwd_tile(tokens, channels);
+    const int64_t tiles = (tokens + tile - 1) / tile;
+    int blocks = 0;
+    ProBwdParams p = {};
+    p.f = pro_params(a.f, 4, tiles, tile, &blocks);
+    float *part = (float *)a.workspace;
+    ColumnSums cs = {};
+    for (int z = 0; z < 3; ++z) {
+        const int W = a.f.heads[z] * a.f.d[z];
+        p.dy[z] = a.dy[z];
+        p.dx[z] = a.dx[z];
+        p.part[z] = part;
+        cs.part[z] = part;
+        cs.out0[z] = a.dweight[z];
+        cs.out1[z] = a.dbias[z];
+        cs.n0[z] = 4 * W;
+        cs.n1[z] = W;
+        part += (size_t)tiles * 5 * W;
+    }
+    for (int z = 0; z < 2; ++z) {
+        p.f.g[z].y = a.dlogit[z];
+        p.f.g[z].dy = a.dgate[z];
+    }
+    if (blocks > 0) {
+        prof_before("gdn2_prologue_bwd", st);
+        hipLaunchKernelGGL((prologue_bwd_kernel<In, Out>), dim3(blocks), dim3(kNT), 0, st, p);
+        prof_after(st);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    cs.parts = (int)tiles;
+    cs.jobs = 3;
+    return launch_column_sums(cs, "gdn2_prologue_reduce", st);
+}
+
+hipError_t launch_prologue_bwd(const PrologueBwdArgs &a, hipStream_t st)
+{
+    if (a.f.bf16) return a.out_bf16 ? prologue_bwd_t<uint16_t, uint16_t>(a, st) : prologue_bwd_t<uint16_t, float>(a, st);
+    return a.out_bf16 ? prologue_bwd_t<float, uint16_t>(a, st) : prologue_bwd_t<float, float>(a, st);
+}
+
+} // namespace gdn2

@@ -353,6 +353,139 @@ int gdn2_chunk_bwd_kept(const void *q, const void *k, const void *v, const float
                         float *db, float *dw, float *dS0, void *workspace, size_t workspace_bytes);
 
 /*
+ * ---- The recurrence over short runs of tokens, states in a pool -------------
+ *
+ * gdn2_recurrent_fwd applies the update and readout to the tokens of N
+ * sequences one after the other, on states that live in a pool of slots: the
+ * serving form between gdn2_decode_step (one token, dense states in order) and
+ * gdn2_chunk_fwd (64-token chunks). It serves continuous batching (one token
+ * a sequence, any slots), draft tokens whose effect must not stay (`commit`;
+ * snilld.dk names state versioning and rollback as what a stateful server
+ * needs) and short prompts. Everything is computed in fp32.
+ *
+ *   q, k       [tokens, HK, dk]     in_dtype; head h of H uses q/k head
+ *                                   h / (H / HK); HK divides H
+ *   v          [tokens, H, dv]      in_dtype
+ *   b, w, log_alpha                 [tokens, H, dk], [tokens, H, dv] (in_dtype)
+ *                                   and [tokens, H, dk] (float), or [tokens, H]
+ *                                   where `gates` has their bit
+ *   state      [slots, H, dk, dv]   float, updated in place
+ *   slot_in    [N] int32, or NULL   the slot sequence i starts from (NULL: i)
+ *   slot_out   [N] int32, or NULL   the slot its kept state goes to (NULL: slot_in)
+ *   commit     [N] int32, or NULL   tokens of sequence i whose effect is kept
+ *                                   (NULL: all of them)
+ *   o          [tokens, H, dv]      out_dtype (GDN2_F32 or GDN2_BF16)
+ *   cu_seqlens [N + 1] int32, or NULL: as in gdn2_chunk_fwd
+ *
+ * slot_in, slot_out, commit and cu_seqlens are device arrays. A slot number
+ * outside [0, slots) means none: the sequence starts from zeros, or its state
+ * is not kept. commit is taken within [0, length]: every token is read out
+ * with all tokens before it applied, and the kept state is the one after the
+ * first commit[i] tokens; an empty sequence, or commit 0, copies slot_in to
+ * slot_out. Several sequences may start from one slot; no slot may be written
+ * by two sequences of a call, nor written by one and read by another. Slots
+ * that no sequence writes, and rows of o behind the last sequence, are left as
+ * they were. Unlike elsewhere, log_alpha may be -infinity (a full forget).
+ * A NaN or infinity in a token reaches that token and later ones of its
+ * sequence, never an earlier token or a prefix kept without it.
+ *
+ * dk, dv in {16, 32, 64, 128}. GDN2_ERR_INVALID also for HK not dividing H,
+ * slots < 1, or slot_in NULL with slots < N.
+ */
+int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float *log_alpha, const void *b,
+                       const void *w, int gates, float *state, const int32_t *slot_in, const int32_t *slot_out,
+                       const int32_t *commit, void *o, const int32_t *cu_seqlens, int B, int T, int N, int H, int HK,
+                       int slots, int dk, int dv, int in_dtype, int out_dtype);
+
+/*
+ * ---- The prologue on its own, and its gradient -------------------------------
+ *
+ * gdn2_prologue_fwd computes what the *_prologue entry points fuse (the
+ * formulas above: short convolutions of q, k, v, unit norm of q and k,
+ * sigmoids of the gate logits) and writes the mixer's inputs, for the entry
+ * points that take those: gdn2_recurrent_fwd, gdn2_chunk_fwd_keep.
+ *
+ *   q_raw, k_raw [tokens, HK, dk], v_raw [tokens, H, dv]   in_dtype
+ *   b_logit [tokens, H, dk], w_logit [tokens, H, dv]       in_dtype, or
+ *                        [tokens, H] where `gates` has GDN2_GATE_B_PER_HEAD /
+ *                        GDN2_GATE_W_PER_HEAD (no other bit)
+ *   conv                 as above, with HK heads for q and k (weight_q
+ *                        [HK*dk, 4]); its histories are pools:
+ *                        state_in / state_out_q [slots, HK, 3, dk] and so on
+ *   slot_in, slot_out, commit   as in gdn2_recurrent_fwd, for the histories:
+ *                        the three raw inputs before the sequence come from
+ *                        slot_in (none: zeros), the last three up to its first
+ *                        commit[i] tokens go to slot_out. state_out_* may be
+ *                        state_in_* (the pools updated in place).
+ *   q, k, v, b, w        shaped like the raw tensors, in_dtype; b and w may be
+ *                        their logits, the others must not overlap an input
+ *
+ * Sizes, cu_seqlens and errors as in gdn2_recurrent_fwd (slots counts only
+ * where a history is given); rows behind the last sequence are left as they
+ * were.
+ */
+int gdn2_prologue_fwd(const void *q_raw, const void *k_raw, const void *v_raw, const void *b_logit,
+                      const void *w_logit, int gates, const gdn2_short_conv *conv, const int32_t *slot_in,
+                      const int32_t *slot_out, const int32_t *commit, void *q, void *k, void *v, void *b, void *w,
+                      const int32_t *cu_seqlens, int B, int T, int N, int H, int HK, int slots, int dk, int dv,
+                      int in_dtype);
+
+/*
+ * Gradient of gdn2_prologue_fwd: from dq, dk_, dv_, db, dw (float, shaped like
+ * q, k, v, b, w, as gdn2_chunk_bwd returns them) those of the raw tensors and
+ * logits (grad_dtype: GDN2_F32 or GDN2_BF16) and of taps and biases (float,
+ * [heads*d, 4] and [heads*d]; the three dbias pointers may each be NULL).
+ * conv: weights, biases and state_in as in the forward (state_out is not
+ * used); histories are taken as constants. No output may overlap an input.
+ * workspace: gdn2_prologue_bwd_workspace_bytes(...) of device memory. The
+ * taps' sums run in a fixed order: the same inputs give the same bits. Rows of
+ * the raw gradients behind the last sequence are left as they were.
+ */
+size_t gdn2_prologue_bwd_workspace_bytes(int B, int T, int N, int H, int HK, int dk, int dv, int varlen);
+int gdn2_prologue_bwd(const void *q_raw, const void *k_raw, const void *v_raw, const void *b_logit,
+                      const void *w_logit, int gates, const gdn2_short_conv *conv, const int32_t *slot_in,
+                      const float *dq, const float *dk_, const float *dv_, const float *db, const float *dw,
+                      void *dq_raw, void *dk_raw, void *dv_raw, void *db_logit, void *dw_logit, float *dweight_q,
+                      float *dweight_k, float *dweight_v, float *dbias_q, float *dbias_k, float *dbias_v,
+                      const int32_t *cu_seqlens, int B, int T, int N, int H, int HK, int slots, int dk, int dv,
+                      int in_dtype, int grad_dtype, void *workspace, size_t workspace_bytes);
+
+/*
+ * ---- LayerNorm(x + residual) and its gradient ---------------------------------
+ *
+ * The layer's closing step, LayerNorm(x + out_proj(y)) (aifetchly, "Gated
+ * DeltaNet-2 Guide", "End-to-End PyTorch Implementation"), over rows of `cols`
+ * elements:
+ *   h = x + residual, y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias
+ *
+ *   x, residual  [rows, cols] in_dtype; residual may be NULL (h = x)
+ *   weight, bias [cols] float; bias may be NULL (none)
+ *   y            [rows, cols] out_dtype
+ *   sum          [rows, cols] in_dtype, or NULL: receives h, rounded
+ * y and sum may each be x or residual itself (same type), but must not overlap
+ * an input otherwise, nor each other. mean and variance are those of the
+ * unrounded h, in fp32.
+ *
+ * gdn2_layer_norm_bwd: from dy = dL/dy (out_dtype of the forward) and h (the
+ * sum the forward wrote, or its x; in_dtype), dh = dL/dh (in_dtype; the
+ * gradient of x and of residual alike), plus dsum (in_dtype) where not NULL:
+ * what else depends on h. dweight, dbias [cols] float are summed over the rows
+ * in a fixed order; dbias may be NULL. dh may be dy, h or dsum itself (same
+ * type). workspace: gdn2_layer_norm_bwd_workspace_bytes(...) of device memory.
+ *
+ * rows >= 0, 1 <= cols <= GDN2_LAYER_NORM_MAX_COLS, eps > 0, each finite.
+ * Pointers are 16-byte aligned; cols may be any number (a multiple of 8 is
+ * faster).
+ */
+#define GDN2_LAYER_NORM_MAX_COLS (1 << 20)
+int gdn2_layer_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias, void *y, void *sum,
+                        int64_t rows, int cols, float eps, int in_dtype, int out_dtype);
+size_t gdn2_layer_norm_bwd_workspace_bytes(int64_t rows, int cols);
+int gdn2_layer_norm_bwd(const void *dy, const void *h, const float *weight, const void *dsum, void *dh, float *dweight,
+                        float *dbias, int64_t rows, int cols, float eps, int in_dtype, int out_dtype, void *workspace,
+                        size_t workspace_bytes);
+
+/*
  * Per-kernel timing, for measurement tools (not needed for computing).
  * gdn2_profile_begin(max_calls) makes this thread's next gdn2_chunk_fwd /
  * gdn2_decode_step calls (up to max_calls of them, 1..4096) record a HIP
