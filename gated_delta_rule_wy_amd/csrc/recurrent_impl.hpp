@@ -8,27 +8,25 @@
 //
 // Tokens go through in blocks of up to 8. With D_t the product of the
 // block's alphas up to t, a block of start state S0 is
-//   A_ts = sum_c (b_t k_t)_c (alpha_{s+1} .. alpha_t)_c (k_s)_c      (t > s)
-//   P_ts = sum_c (q_t)_c (alpha_{s+1} .. alpha_t)_c (k_s)_c          (t >= s)
-//   R_E = (b k D) S0,  R_Q = (q D) S0,  X = (I + A)^-1
+//   A_ts = (b_t k_t D_t) . (k_s / D_s)  (t > s),  P_ts = (q_t D_t) . (k_s / D_s)  (t >= s)
+//   R_E = (b k D) S0, R_Q = (q D) S0, X = (I + A)^-1
 //   Delta = X (U - R_E),  O = R_Q + P X (U - R_E)
 //   S = D_8 S0 + (k alpha_{t+1} .. alpha_8)^T Delta
-// Every decay is a running product of alphas (never a quotient or a
-// difference of logarithms), so any log alpha <= 0 is exact to a few units of
-// the last place, log alpha = -inf (a full forget) among them. All of it is
-// fp32, on the fp32 matrix instruction.
+// Decays are running products of alphas, so log alpha may be anything down to
+// -inf (a full forget); the quotients need D_s >= 2^-100, and a block with
+// less is cut in half, down to a single token, which has none. All of it is
+// fp32, the products on the fp32 matrix instruction.
 //
-// A workgroup owns 16*NC*NW columns of one (sequence, head) state, a wave
-// 16*NC of them in registers: tile r, lane n + 16g holds rows 16r + 4g + j of
-// columns NC*n .. NC*n + NC - 1, which is the accumulator layout, and with
-// element j of a 16-deep fragment on row 4g + j also the right operand's. The
-// block's 16 left rows are ordered so that rows 4g .. 4g+3 are the erase rows
-// of tokens g and g+4 and their query rows: the first product leaves in each
-// lane just what the second one (by [X; P X]) takes as its right operand,
-// which leaves Delta where the third one (by the decayed keys) takes it. The
-// state thus never moves between lanes and is read and written once however
-// many tokens follow, which is what the operator is bound by: 8 bytes a state
-// element.
+// A workgroup of dv/16 waves owns the state of one (sequence, head), a wave 16
+// columns of it in registers: tile r, lane n + 16g holds rows 16r + 4g + j of
+// column n, which is the accumulator layout, and with element j of a 16-deep
+// fragment on row 4g + j also the right operand's. The block's 16 left rows are
+// ordered so that rows 4g .. 4g+3 are the erase rows of tokens g and g+4 and
+// their query rows: the first product leaves in each lane just what the second
+// one (by [X; P X]) takes as its right operand, which leaves Delta where the
+// third one (by the decayed keys) takes it. The state thus never moves between
+// lanes and is read and written once however many tokens follow, which is what
+// the operator is bound by: 8 bytes a state element.
 #pragma once
 
 #include "gdn2_launch.hpp"
@@ -82,17 +80,16 @@ __device__ __forceinline__ void hold_reads() { asm volatile("" ::: "memory"); }
 __device__ __forceinline__ f4 splat4(float x) { f4 r = {x, x, x, x}; return r; }
 
 template <typename In, int DK, int NW>
-__global__ __launch_bounds__(64 * NW, 4) void recurrent_kernel(RecParams a)
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 ? 3 : 4))) void recurrent_kernel(RecParams a)
 {
     constexpr int C = kRecTokens, NT = 64 * NW, NR = DK / 16, DV = 16 * NW;
     constexpr int XS = DK + 4;    // row stride of the fragment tiles (16-byte rows)
-    constexpr int RS = DK + 16;   // row stride of the raw rows: four of them apart in the banks
-    // one thread takes four channels of a token
-    constexpr int C4 = DK / 4, ITEMS = C * C4, IPT = (ITEMS + NT - 1) / NT;
-    __shared__ __align__(16) float sX[16][XS], sKh[C][XS], sG[DK];
-    __shared__ __align__(16) float sK[C][RS], sB[C][RS], sQ[C][RS], sD[C][RS];
-    __shared__ float sPart[NW][4][9][2], sM[16][C + 1];
-    __shared__ int sBad;   // a value of the block's tokens is not finite
+    // A lane takes four channels of a token, a wave 8 tokens of 32 channels
+    constexpr int C4 = DK / 4, NCH = (DK + 31) / 32, IPT = (NCH + NW - 1) / NW;
+    constexpr int NAP = NW < NR ? NW : NR;   // waves that share the products for A and P
+    __shared__ __align__(16) float sX[16][XS], sKi[C][XS], sKh[2][C][XS], sG[2][DK], sPart[NAP][4][C][4];
+    __shared__ float sM[16][C + 1];
+    __shared__ int sBad[2], sWide[2];
 
     const int i = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const int hk = h / (a.H / a.HK);
@@ -184,7 +181,17 @@ __global__ __launch_bounds__(64 * NW, 4) void recurrent_kernel(RecParams a)
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) __builtin_nontemporal_store(S[r][j], sp + (16 * r + j) * DV);
+            for (int j = 0; j < 4; ++j) sp[(16 * r + j) * DV] = S[r][j];
+    };
+    // row `row` (of lane n) of sX times the state, in two chains of products
+    auto left_product = [&](int row) {
+        f4 R[2] = {f4zero(), f4zero()};
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            R[r & 1] = Mma<float>::mma(*reinterpret_cast<const f4 *>(&sX[row][16 * r + 4 * g]), S[r], R[r & 1]);
+            if (r % 4 == 3) hold_reads();
+        }
+        return R[0] + R[1];
     };
     if (commit == 0 && sin != sout) keep();
     if (len == 0) return;   // (no token to load)
@@ -200,193 +207,184 @@ __global__ __launch_bounds__(64 * NW, 4) void recurrent_kernel(RecParams a)
             make_item(x, kk, qq, bb, dd);
             *reinterpret_cast<f4 *>(&sX[0][4 * tid]) = bb * dd;
             *reinterpret_cast<f4 *>(&sX[2][4 * tid]) = qq * dd;
-            *reinterpret_cast<f4 *>(&sKh[0][4 * tid]) = kk;
-            *reinterpret_cast<f4 *>(&sQ[0][4 * tid]) = qq;
-            *reinterpret_cast<f4 *>(&sG[4 * tid]) = dd;
+            *reinterpret_cast<f4 *>(&sKh[0][0][4 * tid]) = kk;
+            *reinterpret_cast<f4 *>(&sKi[0][4 * tid]) = qq;
+            *reinterpret_cast<f4 *>(&sG[0][4 * tid]) = dd;
         }
         __syncthreads();
         float kq = 0.f;
 #pragma unroll
         for (int c = 0; c < DK; c += 64)
-            if (DK >= 64 || lane < DK) kq += sKh[0][c + lane] * sQ[0][c + lane];
+            if (DK >= 64 || lane < DK) kq += sKh[0][0][c + lane] * sKi[0][c + lane];
         kq = lane_group_sum<64>(kq);
         // rows 0 and 2 are the token's; all others repeat one of them
-        f4 R = f4zero();
-#pragma unroll
-        for (int r = 0; r < NR; ++r) R = Mma<float>::mma(*reinterpret_cast<const f4 *>(&sX[n & 2][16 * r + 4 * g]), S[r], R);
+        const f4 R = left_product(n & 2);
         const float d = make_u(cu) - R[0];
         if (commit == 1 && has_out) {
             const float dg = g == 0 ? d : 0.f;
 #pragma unroll
             for (int r = 0; r < NR; ++r)
-                S[r] = mfma4(sKh[0][16 * r + n], dg, S[r] * *reinterpret_cast<const f4 *>(&sG[16 * r + 4 * g]));
+                S[r] = mfma4(sKh[0][0][16 * r + n], dg, S[r] * *reinterpret_cast<const f4 *>(&sG[0][16 * r + 4 * g]));
             keep();
         }
         if (g == 0) put_o(t0, col, R[2] + kq * d);
         return;
     }
 
-    // Tokens of a block. The products multiply what comes after a token by
-    // zeros, which hides any number but a NaN or an infinity: a block that
-    // holds one is done again without the tokens that are not committed, or,
-    // where that is not it, one token at a time, with all that follow it.
-    int most = C, L = 0;
+    // Tokens of a block. A block is done again with fewer tokens where
+    //  - a token holds a NaN or an infinity: the products multiply what comes
+    //    after a token by zeros, which hides any other number. First without a
+    //    draft's end (its committed part stays one block), then token by token;
+    //  - a channel decays by more than 2^100 within it: A and P are formed as
+    //    products of rows decayed from the block's start and keys divided by
+    //    that decay. Half the tokens, down to one, which needs neither.
+    int most = C, L = 0, par = 0;
     // A block ends at the committed prefix, whose state is kept, but for the
     // last one, whose later tokens then leave the state alone.
     auto length = [&](int done) {
         const int rem = len - done;
         return rem <= most ? rem : min(most, done < commit ? commit - done : rem);
     };
-    if (tid == 0) sBad = 0;
     Item x[IPT];
     Col cu[2];
-    auto load_block = [&](int tb, int L, int tid) {
-        const int g = tid >> 4 & 3, col = 16 * wv + (tid & 15);
+    auto load_block = [&](int tb, int L, int lane) {
 #pragma unroll
         for (int m = 0; m < IPT; ++m) {
-            const int it = min(tid + m * NT, ITEMS - 1);
-            load_item(tb + min(it / C4, L - 1), it % C4 * 4, x[m]);
+            const int c = (wv + m * NW) * 32 + (lane & 7) * 4;
+            if (NCH % NW == 0 || wv + m * NW < NCH) load_item(tb + min(lane >> 3, L - 1), DK < 32 ? c % DK : c, x[m]);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) load_u(tb + min(g + 4 * j, L - 1), col, cu[j]);
+        for (int j = 0; j < 2; ++j) load_u(tb + min((lane >> 4) + 4 * j, L - 1), 16 * wv + (lane & 15), cu[j]);
     };
+    // Of the products of d over a channel's 8 tokens (lanes 8 apart): up to the
+    // lane's token, behind it, and of all. Each step joins the groups of
+    // tokens that differ in one bit.
+    auto scan = [&](const f4 &d, f4 &up, f4 &behind, f4 &all, int lane) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float p = d[e], q = 1.f, t = d[e];
+            const float o8 = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(t), 0x128, 0xF, 0xF, false));   // row_ror:8
+            p *= lane & 8 ? o8 : 1.f;
+            q *= lane & 8 ? 1.f : o8;
+            t *= o8;
+            const auto a16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(t), __float_as_uint(t), false, false);
+            const float e16 = __uint_as_float(a16[0]), f16 = __uint_as_float(a16[1]);   // of the even row, of the odd one
+            p *= lane & 16 ? e16 : 1.f;
+            q *= lane & 16 ? 1.f : f16;
+            t = e16 * f16;
+            const auto a32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(t), __float_as_uint(t), false, false);
+            const float e32 = __uint_as_float(a32[0]), f32 = __uint_as_float(a32[1]);
+            p *= lane & 32 ? e32 : 1.f;
+            q *= lane & 32 ? 1.f : f32;
+            up[e] = p;
+            behind[e] = q;
+            all[e] = e32 * f32;
+        }
+    };
+    if (tid < 2) sBad[tid] = sWide[tid] = 0;
     L = length(0);
-    load_block(t0, L, tid);
+    load_block(t0, L, lane);
     __syncthreads();
-    for (int done = 0; done < len;) {
+    for (int done = 0; done < len; par ^= 1) {
         int lane = tid & 63;
         // (the lane's addresses are formed anew in each block: kept over the
         // loop they would take a third of the registers)
         asm volatile("" : "+v"(lane));
-        const int tid = wv * 64 + lane, n = lane & 15, g = lane >> 4, col = 16 * wv + n;
+        const int n = lane & 15, g = lane >> 4, col = 16 * wv + n;
         const int tb = t0 + done;
-        f4 kk[IPT], qq[IPT], bb[IPT];
-        float U[2];
-        for (;;) {
-            // ---- raw rows; those past the block are zeros that decay nothing
-            float bad = 0.f;
-#pragma unroll
-            for (int m = 0; m < IPT; ++m) {
-                const int it = tid + m * NT, t = it / C4, c = it % C4 * 4;
-                f4 dd;
-                make_item(x[m], kk[m], qq[m], bb[m], dd);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    kk[m][e] = t < L ? kk[m][e] : 0.f;
-                    qq[m][e] = t < L ? qq[m][e] : 0.f;
-                    bb[m][e] = t < L ? bb[m][e] : 0.f;
-                    dd[e] = t < L ? dd[e] : 1.f;
-                    bad += 0.f * (kk[m][e] + qq[m][e] + bb[m][e] + dd[e]);
-                }
-                if (ITEMS % NT == 0 || it < ITEMS) {
-                    *reinterpret_cast<f4 *>(&sK[t][c]) = kk[m];
-                    *reinterpret_cast<f4 *>(&sQ[t][c]) = qq[m];
-                    *reinterpret_cast<f4 *>(&sB[t][c]) = bb[m];
-                    *reinterpret_cast<f4 *>(&sD[t][c]) = dd;
-                }
-            }
-            // U = w*v of this lane's column, tokens g and g + 4
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                U[j] = g + 4 * j < L ? make_u(cu[j]) : 0.f;
-                bad += 0.f * U[j];
-            }
-            if (L > 1 && bad != 0.f) sBad = 1;   // (0 x: NaN unless x is finite)
-            __syncthreads();
-            if (L == 1 || !sBad) break;
-            // (first without a draft's end: its committed part stays one block)
-            if (done < commit && commit < done + L) L = commit - done;
-            else most = L = 1;
-            load_block(tb, L, tid);
-            __syncthreads();
-            if (tid == 0) sBad = 0;
-        }
-        // the block's tokens whose effect stays: all but those of a draft's end
+        // ---- the block's rows; tokens past it are zeros that decay nothing
+        // (those whose effect stays: all but those of a draft's end)
         const int stay = done + L < len ? L : min(max(commit - done, 0), L);
-        // the next block's loads, under way during this one's products
-        const int next = done + L;
-        const int Lb = L;
-        if (next < len) {
-            L = length(next);
-            load_block(t0 + next, L, tid);
-        }
-
-        // ---- the decayed rows: products of alphas up to a token and behind it
+        float bad = 0.f;
+        bool wide = false;
 #pragma unroll
         for (int m = 0; m < IPT; ++m) {
-            const int it = tid + m * NT, t = it / C4, c = it % C4 * 4;
-            if (ITEMS % NT != 0 && it >= ITEMS) break;
-            f4 up = splat4(1.f), on = splat4(1.f), all = splat4(1.f);
+            const int t = lane >> 3, c = (wv + m * NW) * 32 + (lane & 7) * 4;
+            if (NCH % NW != 0 && wv + m * NW >= NCH) break;
+            f4 kk, qq, bb, dd, up, on, all;
+            make_item(x[m], kk, qq, bb, dd);
+            // (a token alone: its query, undecayed, in the next one's row too, for q.k)
+            const bool alone = L == 1 && t == 1;
 #pragma unroll
-            for (int s = 0; s < C; ++s) {
-                const f4 d = *reinterpret_cast<const f4 *>(&sD[s][c]);
+            for (int e = 0; e < 4; ++e) {
+                kk[e] = t < L ? kk[e] : 0.f;
+                qq[e] = t < L || alone ? qq[e] : 0.f;
+                bb[e] = t < L ? bb[e] : 0.f;
+                dd[e] = t < L ? dd[e] : 1.f;
+                bad += 0.f * (kk[e] + qq[e] + bb[e] + dd[e]);
+            }
+            scan(dd, up, on, all, lane);
+            f4 ki;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                wide = wide || !(up[e] >= 0x1p-100f);
+                ki[e] = L > 1 ? kk[e] * __builtin_amdgcn_rcpf(up[e]) : kk[e];
+            }
+            if (stay < L) {
+                f4 none;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    up[e] *= s <= t ? d[e] : 1.f;
-                    on[e] *= s > t && s < stay ? d[e] : 1.f;
-                    all[e] *= s < stay ? d[e] : 1.f;
+                    kk[e] = t < stay ? kk[e] : 0.f;
+                    dd[e] = t < stay ? dd[e] : 1.f;
                 }
-                if (s == 3) hold_reads();
+                scan(dd, none, on, all, lane);
             }
-            *reinterpret_cast<f4 *>(&sX[rec_row(t)][c]) = bb[m] * up;
-            *reinterpret_cast<f4 *>(&sX[rec_row(t) + 2][c]) = qq[m] * up;
-            *reinterpret_cast<f4 *>(&sKh[t][c]) = t < stay ? kk[m] * on : f4zero();
-            if (t == C - 1) *reinterpret_cast<f4 *>(&sG[c]) = all;
+            if (DK >= 32 || c < DK) {
+                *reinterpret_cast<f4 *>(&sX[rec_row(t)][c]) = bb * up;
+                *reinterpret_cast<f4 *>(&sX[rec_row(t) + 2][c]) = alone ? qq : qq * up;
+                *reinterpret_cast<f4 *>(&sKi[t][c]) = ki;
+                *reinterpret_cast<f4 *>(&sKh[par][t][c]) = kk * on;
+                if (t == 0) *reinterpret_cast<f4 *>(&sG[par][c]) = all;
+            }
+        }
+        // U = w*v of this lane's column, tokens g and g + 4
+        float U[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            U[j] = g + 4 * j < L ? make_u(cu[j]) : 0.f;
+            bad += 0.f * U[j];
+        }
+        if (bad != 0.f) sBad[par] = 1;   // (0 x: NaN unless x is finite)
+        if (wide) sWide[par] = 1;
+        __syncthreads();
+        if (L > 1 && (sBad[par] || sWide[par])) {
+            if (!sBad[par]) most = L = L / 2;
+            else if (done < commit && commit < done + L) L = commit - done;
+            else most = L = 1;
+            load_block(tb, L, lane);
+            if (tid == 0) sBad[par ^ 1] = sWide[par ^ 1] = 0;
+            __syncthreads();
+            continue;
+        }
+        if (tid == 0) sBad[par ^ 1] = sWide[par ^ 1] = 0;
+        // the next block's loads, under way during this one's products
+        const int next = done + L, Lb = L;
+        if (next < len) {
+            L = length(next);
+            load_block(t0 + next, L, lane);
         }
 
-        // ---- A and P: lane group p of 16 takes columns s = p and 7 - p of
-        // the triangle (9 entries), its lanes and the waves share the channels
-        {
-            const int p = g;
-            float ea[9], ep[9];
+        // ---- A and P: the decayed rows by the keys over their decays; lane n
+        // (of 8) + 16 g has A and P of tokens g and g + 4 with token n
+        if (NAP == NW || wv < NAP) {
+            f4 ap = f4zero();
 #pragma unroll
-            for (int e = 0; e < 9; ++e) ea[e] = ep[e] = 0.f;
-#pragma unroll
-            for (int c0 = 0; c0 < DK; c0 += 16 * NW) {
-                const int c = c0 + wv * 16 + n;
-                if (DK % (16 * NW) != 0 && c >= DK) break;
-                float kf = 0.f;
-#pragma unroll
-                for (int e = 0; e < 9; ++e) {
-                    const int t = e < 8 - p ? p + e : e - 1;
-                    // the pair's first entry is (s, s); the factor then runs on
-                    const float kx = sK[t][c], dx = sD[t][c];
-                    kf = e == 0 || e == 8 - p ? kx : kf * dx;
-                    ea[e] += sB[t][c] * kf;
-                    ep[e] += sQ[t][c] * kf;
-                    if (e == 4) hold_reads();
-                }
-                hold_reads();
+            for (int r0 = 0; r0 < NR; r0 += NAP) {
+                const int at = 16 * (r0 + wv) + 4 * g;
+                ap = Mma<float>::mma(*reinterpret_cast<const f4 *>(&sX[n][at]), *reinterpret_cast<const f4 *>(&sKi[n & 7][at]), ap);
             }
-#pragma unroll
-            for (int e = 0; e < 9; ++e) {
-                ea[e] = lane_group_sum<16>(ea[e]);
-                ep[e] = lane_group_sum<16>(ep[e]);
-            }
-            if (n == 0)
-#pragma unroll
-                for (int e = 0; e < 9; ++e) {
-                    sPart[wv][p][e][0] = ea[e];
-                    sPart[wv][p][e][1] = ep[e];
-                }
+            if (n < C) *reinterpret_cast<f4 *>(&sPart[wv][g][n][0]) = ap;
         }
         __syncthreads();
 
-        // ---- [X; P X] by wave 0, a column a lane: lane 9 p + e has an entry
-        // of A and one of P, which go to all lanes as scalars
+        // ---- [X; P X] by wave 0, a column a lane; the entries of A and P go
+        // to all lanes as scalars
         if (wv == 0) {
-            float xa = 0.f, xp = 0.f;
-            if (lane < 36) {
-                const int p = lane / 9, e = lane % 9;
+            f4 ap = f4zero();
 #pragma unroll
-                for (int z = 0; z < NW; ++z) {
-                    xa += sPart[z][p][e][0];
-                    xp += sPart[z][p][e][1];
-                }
-            }
-            auto entry = [](float f, int t, int s) {
-                const int at = s < 4 ? 9 * s + t - s : 9 * (7 - s) + t + 1;
-                return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), at));
+            for (int z = 0; z < NAP; ++z) ap += *reinterpret_cast<const f4 *>(&sPart[z][g][n & 7][0]);
+            auto entry = [&](int what, int t, int s) {
+                return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ap[what + (t >> 2)]), 16 * (t & 3) + s));
             };
             const int j = lane & 7;
             float y[C];
@@ -395,26 +393,17 @@ __global__ __launch_bounds__(64 * NW, 4) void recurrent_kernel(RecParams a)
                 float z = 0.f;
                 y[t] = t == j ? 1.f : 0.f;
 #pragma unroll
-                for (int s = 0; s < t; ++s) y[t] -= entry(xa, t, s) * y[s];
+                for (int s = 0; s < t; ++s) y[t] -= entry(0, t, s) * y[s];
 #pragma unroll
-                for (int s = 0; s <= t; ++s) z += entry(xp, t, s) * y[s];
+                for (int s = 0; s <= t; ++s) z += (t == 0 && Lb == 1 ? entry(2, 1, 0) : entry(2, t, s)) * y[s];
                 if (lane < C) {
                     sM[rec_row(t)][j] = y[t];
                     sM[rec_row(t) + 2][j] = z;
                 }
             }
         }
-        // ---- R = [b k D; q D] S0 (all waves, no wait for the above), in two
-        // chains of products
-        f4 R = f4zero(), R2 = f4zero();
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const f4 z = *reinterpret_cast<const f4 *>(&sX[n][16 * r + 4 * g]);
-            if (r % 2 == 0) R = Mma<float>::mma(z, S[r], R);
-            else R2 = Mma<float>::mma(z, S[r], R2);
-            if (r % 4 == 3) hold_reads();
-        }
-        R += R2;
+        // ---- R = [b k D; q D] S0 (all waves, no wait for the above)
+        f4 R = left_product(n);
         __syncthreads();
 
         // ---- Delta and O, then the state
@@ -426,8 +415,9 @@ __global__ __launch_bounds__(64 * NW, 4) void recurrent_kernel(RecParams a)
         if (stay > 0)
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                S[r] = mfma4(sKh[g + 4][16 * r + n], R[1],
-                             mfma4(sKh[g][16 * r + n], R[0], S[r] * *reinterpret_cast<const f4 *>(&sG[16 * r + 4 * g])));
+                S[r] = mfma4(sKh[par][g + 4][16 * r + n], R[1],
+                             mfma4(sKh[par][g][16 * r + n], R[0],
+                                   S[r] * *reinterpret_cast<const f4 *>(&sG[par][16 * r + 4 * g])));
                 if (r % 4 == 3) hold_reads();
             }
 #pragma unroll
@@ -435,8 +425,8 @@ __global__ __launch_bounds__(64 * NW, 4) void recurrent_kernel(RecParams a)
             if (g + 4 * j < Lb) put_o(tb + g + 4 * j, col, R[2 + j]);
         if (stay > 0 && done + stay == commit) keep();
         done = next;
-        // No barrier: the next block's raw rows are read last before the second
-        // barrier above, and what the products here read is written after its first.
+        // No barrier: what the products here read (sKh, sG: one of two) is
+        // written again two blocks on, the rest after this block's last barrier.
     }
 }
 
