@@ -10,7 +10,7 @@
 // block's alphas up to t, a block of start state S0 is
 //   A_ts = (b_t k_t D_t) . (k_s / D_s)  (t > s),  P_ts = (q_t D_t) . (k_s / D_s)  (t >= s)
 //   R_E = (b k D) S0, R_Q = (q D) S0, X = (I + A)^-1
-//   Delta = X (U - R_E),  O = R_Q + P X (U - R_E)
+//   Delta = X (U - R_E),  O = R_Q + P Delta
 //   S = D_8 S0 + (k alpha_{t+1} .. alpha_8)^T Delta
 // Decays are running products of alphas, so log alpha may be anything down to
 // -inf (a full forget); the quotients need D_s >= 2^-100, and a block with
@@ -23,7 +23,7 @@
 // fragment on row 4g + j also the right operand's. The block's 16 left rows are
 // ordered so that rows 4g .. 4g+3 are the erase rows of tokens g and g+4 and
 // their query rows: the first product leaves in each lane just what the second
-// one (by [X; P X]) takes as its right operand, which leaves Delta where the
+// one (by X, then P,) takes as its right operand, which leaves Delta where the
 // third one (by the decayed keys) takes it. The state thus never moves between
 // lanes and is read and written once however many tokens follow, which is what
 // the operator is bound by: 8 bytes a state element.
@@ -31,6 +31,8 @@
 
 #include "gdn2_launch.hpp"
 #include "rows.hpp"
+
+#include <type_traits>
 
 namespace gdn2 {
 
@@ -53,26 +55,22 @@ struct RecParams {
     int T, H, HK, slots, gates, out_bf16;
 };
 
-// Four elements as they lie in memory (or the first of them alone).
+// Four elements as they lie in memory.
 template <typename In> struct Raw4;
 template <> struct Raw4<uint16_t> {
     uint2 r;
     __device__ __forceinline__ void load(const uint16_t *p) { r = *reinterpret_cast<const uint2 *>(p); }
-    __device__ __forceinline__ void load1(const uint16_t *p) { r.x = *p; }
     __device__ __forceinline__ f4 get() const
     {
         f4 x = {__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
                 __uint_as_float(r.y & 0xFFFF0000u)};
         return x;
     }
-    __device__ __forceinline__ float get1() const { return __uint_as_float(r.x << 16); }
 };
 template <> struct Raw4<float> {
     f4 r;
     __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const f4 *>(p); }
-    __device__ __forceinline__ void load1(const float *p) { r[0] = *p; }
     __device__ __forceinline__ f4 get() const { return r; }
-    __device__ __forceinline__ float get1() const { return r[0]; }
 };
 // Keeps the LDS reads behind it from being issued before it, where that would
 // take more registers than there are.
@@ -89,7 +87,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
     constexpr int NAP = NW < NR ? NW : NR;   // waves that share the products for A and P
     __shared__ __align__(16) float sX[16][XS], sKi[C][XS], sKh[2][C][XS], sG[2][DK], sPart[NAP][4][C][4];
     __shared__ float sM[16][C + 1];
-    __shared__ int sBad[2], sWide[2];
+    __shared__ int2 sFlag[2];   // of even and odd blocks: x: a value is not finite, y: a wide decay
 
     const int i = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const int hk = h / (a.H / a.HK);
@@ -124,40 +122,58 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
     struct Item {
         Raw4<In> k, q, b;
         f4 la;
+        In b1;       // gates of one value a head
+        float la1;
     };
-    // the four channels at c of token tok
-    auto load_item = [&](int tok, int c, Item &x) {
-        const size_t ih = (size_t)tok * a.H + h, ik = ((size_t)tok * a.HK + hk) * DK + c, ic = ih * DK + c;
-        x.k.load(k + ik);
-        x.q.load(q + ik);
-        if (bsc) x.b.load1(b + ih);
-        else x.b.load(b + ic);
-        if (asc) x.la[0] = a.la[ih];
-        else x.la = *reinterpret_cast<const f4 *>(a.la + ic);
+    // A token's rows lie a scalar base and a small lane offset away: `off`
+    // tokens behind token tok (the same for the workgroup).
+    const int wk = a.HK * DK, wh = a.H * DK, wvw = a.H * DV;
+    // (in bytes: 32 of them are enough for a block)
+    auto at = [](auto *p, unsigned n) {
+        using T = std::remove_reference_t<decltype(*p)>;
+        using B = std::conditional_t<std::is_const_v<T>, const char, char>;
+        return reinterpret_cast<T *>(reinterpret_cast<B *>(p) + n * (unsigned)sizeof(T));
+    };
+    // the four channels at c. Both forms of a gate are loaded, the one that is
+    // not there from rows that are: a branch around a load would make the
+    // wave wait for it there.
+    auto load_item = [&](int tok, int off, int c, Item &x) {
+        const size_t ih = (size_t)tok * a.H + h, ik = ((size_t)tok * a.HK + hk) * DK;
+        const unsigned ok = off * wk + c, oh = off * wh + c, o1 = off * a.H;
+        x.k.load(at(k + ik, ok));
+        x.q.load(at(q + ik, ok));
+        x.b.load(at(bsc ? k + ik : b + ih * DK, bsc ? ok : oh));
+        x.b1 = *at(bsc ? b + ih : k + ik, bsc ? o1 : 0);
+        x.la = *reinterpret_cast<const f4 *>(at(asc ? a.state : a.la + ih * DK, asc ? 0 : oh));
+        x.la1 = *at(a.la + (asc ? ih : ih * DK), asc ? o1 : 0);
     };
     // k, q, b*k and alpha
     auto make_item = [&](const Item &x, f4 &kk, f4 &qq, f4 &bb, f4 &dd) {
         kk = x.k.get();
         qq = x.q.get();
-        bb = (bsc ? splat4(x.b.get1()) : x.b.get()) * kk;
-        const f4 la = asc ? splat4(x.la[0]) : x.la;
+        const f4 bw = x.b.get();
+        const float b1 = in2f<In>(x.b1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dd[e] = __expf(la[e]);
+        for (int e = 0; e < 4; ++e) {
+            bb[e] = (bsc ? b1 : bw[e]) * kk[e];
+            dd[e] = __expf(asc ? x.la1 : x.la[e]);
+        }
     };
     // v and w of this lane's column
     struct Col {
         In v, w;
     };
-    auto load_u = [&](int tok, int col, Col &x) {
+    auto load_u = [&](int tok, int off, int col, Col &x) {
         const size_t ih = (size_t)tok * a.H + h;
-        x.v = v[ih * DV + col];
-        x.w = w[wsc ? ih : ih * DV + col];
+        x.v = *at(v + ih * DV, off * wvw + col);
+        x.w = *at(w + (wsc ? ih : ih * DV), wsc ? off * a.H : off * wvw + col);
     };
     auto make_u = [&](const Col &x) { return in2f<In>(x.v) * in2f<In>(x.w); };
-    auto put_o = [&](int tok, int col, float x) {
-        const size_t io = ((size_t)tok * a.H + h) * DV + col;
-        if (a.out_bf16) ((uint16_t *)a.o)[io] = (uint16_t)bf16x2(x, 0.f);
-        else ((float *)a.o)[io] = x;
+    auto put_o = [&](int tok, int off, int col, float x) {
+        const size_t io = ((size_t)tok * a.H + h) * DV;
+        const unsigned to = off * wvw + col;
+        if (a.out_bf16) *at((uint16_t *)a.o + io, to) = (uint16_t)bf16x2(x, 0.f);
+        else *at((float *)a.o + io, to) = x;
     };
 
     const size_t own = (size_t)h * DK * DV, slot_sz = (size_t)a.H * DK * DV;
@@ -189,7 +205,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             R[r & 1] = Mma<float>::mma(*reinterpret_cast<const f4 *>(&sX[row][16 * r + 4 * g]), S[r], R[r & 1]);
-            if (r % 4 == 3) hold_reads();
         }
         return R[0] + R[1];
     };
@@ -199,11 +214,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
     if (len == 1) {
         // ---- a single token: Delta = U - R_E, O = R_Q + (q.k) Delta
         Col cu;
-        load_u(t0, col, cu);
+        load_u(t0, 0, col, cu);
         if (tid < C4) {
             Item x;
             f4 kk, qq, bb, dd;
-            load_item(t0, 4 * tid, x);
+            load_item(t0, 0, 4 * tid, x);
             make_item(x, kk, qq, bb, dd);
             *reinterpret_cast<f4 *>(&sX[0][4 * tid]) = bb * dd;
             *reinterpret_cast<f4 *>(&sX[2][4 * tid]) = qq * dd;
@@ -227,7 +242,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
                 S[r] = mfma4(sKh[0][0][16 * r + n], dg, S[r] * *reinterpret_cast<const f4 *>(&sG[0][16 * r + 4 * g]));
             keep();
         }
-        if (g == 0) put_o(t0, col, R[2] + kq * d);
+        if (g == 0) put_o(t0, 0, col, R[2] + kq * d);
         return;
     }
 
@@ -251,10 +266,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
 #pragma unroll
         for (int m = 0; m < IPT; ++m) {
             const int c = (wv + m * NW) * 32 + (lane & 7) * 4;
-            if (NCH % NW == 0 || wv + m * NW < NCH) load_item(tb + min(lane >> 3, L - 1), DK < 32 ? c % DK : c, x[m]);
+            if (NCH % NW == 0 || wv + m * NW < NCH) load_item(tb, min(lane >> 3, L - 1), DK < 32 ? c % DK : c, x[m]);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) load_u(tb + min((lane >> 4) + 4 * j, L - 1), 16 * wv + (lane & 15), cu[j]);
+        for (int j = 0; j < 2; ++j) load_u(tb, min((lane >> 4) + 4 * j, L - 1), 16 * wv + (lane & 15), cu[j]);
     };
     // Of the products of d over a channel's 8 tokens (lanes 8 apart): up to the
     // lane's token, behind it, and of all. Each step joins the groups of
@@ -281,7 +296,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
             all[e] = e32 * f32;
         }
     };
-    if (tid < 2) sBad[tid] = sWide[tid] = 0;
+    if (tid < 2) sFlag[tid] = make_int2(0, 0);
     L = length(0);
     load_block(t0, L, lane);
     __syncthreads();
@@ -315,9 +330,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
             }
             scan(dd, up, on, all, lane);
             f4 ki;
+            wide = wide || !(fminf(fminf(up[0], up[1]), fminf(up[2], up[3])) >= 0x1p-100f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                wide = wide || !(up[e] >= 0x1p-100f);
                 ki[e] = L > 1 ? kk[e] * __builtin_amdgcn_rcpf(up[e]) : kk[e];
             }
             if (stay < L) {
@@ -344,19 +359,21 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
             U[j] = g + 4 * j < L ? make_u(cu[j]) : 0.f;
             bad += 0.f * U[j];
         }
-        if (bad != 0.f) sBad[par] = 1;   // (0 x: NaN unless x is finite)
-        if (wide) sWide[par] = 1;
+        if (bad != 0.f) sFlag[par].x = 1;   // (0 x: NaN unless x is finite)
+        if (wide) sFlag[par].y = 1;
         __syncthreads();
-        if (L > 1 && (sBad[par] || sWide[par])) {
-            if (!sBad[par]) most = L = L / 2;
+        // (one value for all: the block's bounds stay in scalar registers)
+        const int bads = __builtin_amdgcn_readfirstlane(sFlag[par].x), wides = __builtin_amdgcn_readfirstlane(sFlag[par].y);
+        if (L > 1 && (bads | wides)) {
+            if (!bads) most = L = L / 2;
             else if (done < commit && commit < done + L) L = commit - done;
             else most = L = 1;
             load_block(tb, L, lane);
-            if (tid == 0) sBad[par ^ 1] = sWide[par ^ 1] = 0;
+            if (tid == 0) sFlag[par ^ 1] = make_int2(0, 0);
             __syncthreads();
             continue;
         }
-        if (tid == 0) sBad[par ^ 1] = sWide[par ^ 1] = 0;
+        if (tid == 0) sFlag[par ^ 1] = make_int2(0, 0);
         // the next block's loads, under way during this one's products
         const int next = done + L, Lb = L;
         if (next < len) {
@@ -377,52 +394,59 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
         }
         __syncthreads();
 
-        // ---- [X; P X] by wave 0, a column a lane; the entries of A and P go
-        // to all lanes as scalars
+        // ---- X and P by wave 0 (X a column a lane, the entries of A as
+        // scalars), R = [b k D; q D] S0 by all
         if (wv == 0) {
             f4 ap = f4zero();
 #pragma unroll
             for (int z = 0; z < NAP; ++z) ap += *reinterpret_cast<const f4 *>(&sPart[z][g][n & 7][0]);
-            auto entry = [&](int what, int t, int s) {
-                return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ap[what + (t >> 2)]), 16 * (t & 3) + s));
-            };
             const int j = lane & 7;
+            if (n < C) {
+                sM[rec_row(g) + 2][j] = j <= g ? ap[2] : 0.f;
+                sM[rec_row(g + 4) + 2][j] = j <= g + 4 ? ap[3] : 0.f;
+            }
+            auto entry = [&](int t, int s) {
+                return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ap[t >> 2]), 16 * (t & 3) + s));
+            };
             float y[C];
 #pragma unroll
             for (int t = 0; t < C; ++t) {
-                float z = 0.f;
                 y[t] = t == j ? 1.f : 0.f;
 #pragma unroll
-                for (int s = 0; s < t; ++s) y[t] -= entry(0, t, s) * y[s];
-#pragma unroll
-                for (int s = 0; s <= t; ++s) z += (t == 0 && Lb == 1 ? entry(2, 1, 0) : entry(2, t, s)) * y[s];
-                if (lane < C) {
-                    sM[rec_row(t)][j] = y[t];
-                    sM[rec_row(t) + 2][j] = z;
-                }
+                for (int s = 0; s < t; ++s) y[t] -= entry(t, s) * y[s];
+                sM[rec_row(t)][j] = y[t];   // (eight lanes write the same)
             }
+            if (Lb == 1) sM[rec_row(0) + 2][0] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ap[2]), 16));
         }
-        // ---- R = [b k D; q D] S0 (all waves, no wait for the above)
         f4 R = left_product(n);
+        // the state's decay, while wave 0 works
+        if (stay > 0)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                S[r] *= *reinterpret_cast<const f4 *>(&sG[par][16 * r + 4 * g]);
+                if (r % 4 == 3) hold_reads();
+            }
         __syncthreads();
 
-        // ---- Delta and O, then the state
+        // ---- Delta = X (U - R_E), O = R_Q + P Delta, then the state
         {
+            const float m0 = sM[n][g], m1 = sM[n][g + 4];
+            const bool query = n & 2;
             f4 z = {0.f, 0.f, R[2], R[3]};
-            z = mfma4(sM[n][g], U[0] - R[0], z);
-            R = mfma4(sM[n][g + 4], U[1] - R[1], z);
+            z = mfma4(query ? 0.f : m0, U[0] - R[0], z);
+            z = mfma4(query ? 0.f : m1, U[1] - R[1], z);
+            R = mfma4(query ? m0 : 0.f, z[0], z);
+            R = mfma4(query ? m1 : 0.f, z[1], R);
         }
         if (stay > 0)
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                S[r] = mfma4(sKh[par][g + 4][16 * r + n], R[1],
-                             mfma4(sKh[par][g][16 * r + n], R[0],
-                                   S[r] * *reinterpret_cast<const f4 *>(&sG[par][16 * r + 4 * g])));
+                S[r] = mfma4(sKh[par][g + 4][16 * r + n], R[1], mfma4(sKh[par][g][16 * r + n], R[0], S[r]));
                 if (r % 4 == 3) hold_reads();
             }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            if (g + 4 * j < Lb) put_o(tb + g + 4 * j, col, R[2 + j]);
+            if (g + 4 * j < Lb) put_o(tb, g + 4 * j, col, R[2 + j]);
         if (stay > 0 && done + stay == commit) keep();
         done = next;
         // No barrier: what the products here read (sKh, sG: one of two) is
