@@ -72,10 +72,6 @@ template <> struct Raw4<float> {
     __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const f4 *>(p); }
     __device__ __forceinline__ f4 get() const { return r; }
 };
-// Keeps the LDS reads behind it from being issued before it, where that would
-// take more registers than there are.
-__device__ __forceinline__ void hold_reads() { asm volatile("" ::: "memory"); }
-__device__ __forceinline__ f4 splat4(float x) { f4 r = {x, x, x, x}; return r; }
 
 template <typename In, int DK, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 ? 3 : 4))) void recurrent_kernel(RecParams a)
@@ -424,7 +420,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 S[r] *= *reinterpret_cast<const f4 *>(&sG[par][16 * r + 4 * g]);
-                if (r % 4 == 3) hold_reads();
             }
         __syncthreads();
 
@@ -442,7 +437,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 S[r] = mfma4(sKh[par][g + 4][16 * r + n], R[1], mfma4(sKh[par][g][16 * r + n], R[0], S[r]));
-                if (r % 4 == 3) hold_reads();
             }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
