@@ -10,7 +10,7 @@
 //   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
 //
 // A row is read once and held in registers by TPR threads (a part of a wave,
-// a wave or a workgroup), E packs of V elements each; mean and variance are
+// a wave or a workgroup), E packs of eight elements each; mean and variance are
 // two passes over the registers, so an offset far from zero costs no
 // precision. Rows pass through once, so they are loaded and stored past the
 // caches (non-temporal: 65536 x 2048 bf16 with residual and sum 201 -> 193 us,
@@ -35,44 +35,61 @@ template <int TPR> struct RowShape {
     static constexpr int RPB = NT / TPR;               // rows of a workgroup
 };
 
-template <typename In, typename Out, int V, int TPR, int E, bool RES>
+// What a lane holds: pack e of thread p of a row, n(e) elements of it there
+// (AL: all eight or none).
+template <int TPR, bool AL> struct RowPart {
+    int p, cols;
+    __device__ __forceinline__ int col(int e) const { return (p + e * TPR) * 8; }
+    __device__ __forceinline__ int n(int e) const { return cols - col(e); }
+    __device__ __forceinline__ bool has(int e, int i) const { return (AL ? col(e) : col(e) + i) < cols; }
+    template <bool NT = true, typename T> __device__ __forceinline__ void load(Pack8<T> &x, const T *row, int e) const
+    {
+        x.zero();
+        if (n(e) > 0) x.template load<AL, NT>(row + col(e), n(e));
+    }
+    template <typename T> __device__ __forceinline__ void store(T *row, const float (&x)[8], int e) const
+    {
+        if (n(e) > 0) store8<AL>(row + col(e), x, n(e));
+    }
+};
+
+template <typename In, typename Out, bool AL, int TPR, int E, bool RES>
 __global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_fwd_kernel(
     const In *x, const In *res, const float *__restrict__ weight, const float *__restrict__ bias, Out *y, In *sum,
     int64_t rows, int cols, float inv_n, float eps)
 {
     constexpr int RPB = RowShape<TPR>::RPB;
     __shared__ float red[TPR > 64 ? TPR / 64 : 1];
-    const int p = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    float wv[E][V], bv[E][V];
+    const int grp = threadIdx.x / TPR;
+    const RowPart<TPR, AL> part = {(int)threadIdx.x % TPR, cols};
+    float wv[E][8], bv[E][8];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int c = (p + e * TPR) * V;
+        Pack8<float> pw, pb;
+        part.template load<false>(pw, weight, e);
+        pb.zero();
+        if (bias) part.template load<false>(pb, bias, e);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            wv[e][i] = c < cols ? weight[c + i] : 0.f;
-            bv[e][i] = c < cols && bias ? bias[c + i] : 0.f;
+        for (int i = 0; i < 8; ++i) {
+            wv[e][i] = pw.get(i);
+            bv[e][i] = pb.get(i);
         }
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
         // groups past the last row repeat it and store nothing
         const bool live = r0 + grp < rows;
         const int64_t base = (live ? r0 + grp : rows - 1) * (int64_t)cols;
-        Pack<In, V> px[E], pr[E];
+        Pack8<In> px[E], pr[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int c = (p + e * TPR) * V;
-            px[e].zero();
-            if (RES) pr[e].zero();
-            if (c < cols) {
-                px[e].load_nt(x + base + c);
-                if (RES) pr[e].load_nt(res + base + c);
-            }
+            part.load(px[e], x + base, e);
+            if (RES) part.load(pr[e], res + base, e);
         }
-        float h[E][V], s[1] = {0.f};
+        float h[E][8], s[1] = {0.f};
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 h[e][i] = RES ? px[e].get(i) + pr[e].get(i) : px[e].get(i);
                 s[0] += h[e][i];
             }
@@ -81,22 +98,18 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_fwd_kernel(
         s[0] = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if ((p + e * TPR) * V < cols)
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[0] += (h[e][i] - mean) * (h[e][i] - mean);
+            for (int i = 0; i < 8; ++i) s[0] += part.has(e, i) ? (h[e][i] - mean) * (h[e][i] - mean) : 0.f;
         row_sums<TPR>(s, red);
         const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
         if (live)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int c = (p + e * TPR) * V;
-                if (c < cols) {
-                    float o[V];
+                float o[8];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = (h[e][i] - mean) * rstd * wv[e][i] + bv[e][i];
-                    store_row<V, true>(y + base + c, o);
-                    if (sum) store_row<V, true>(sum + base + c, h[e]);
-                }
+                for (int i = 0; i < 8; ++i) o[i] = (h[e][i] - mean) * rstd * wv[e][i] + bv[e][i];
+                part.store(y + base, o, e);
+                if (sum) part.store(sum + base, h[e], e);
             }
     }
 }
@@ -121,53 +134,49 @@ __global__ __launch_bounds__(1024) void ln_fwd_long_kernel(
         const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
         for (int c = threadIdx.x; c < cols; c += 1024) {
             const float h = at(c), o = (h - mean) * rstd * weight[c] + (bias ? bias[c] : 0.f);
-            store_row<1>(y + base + c, &o);
-            if (sum) store_row<1>(sum + base + c, &h);
+            store1(y + base + c, o);
+            if (sum) store1(sum + base + c, h);
         }
     }
 }
 
 // Gradient. part: [gridDim.x][2][cols], this workgroup's sums of dy xh and dy.
-template <typename In, typename Dy, int V, int TPR, int E, bool SUM>
-__global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_bwd_kernel(
-    const Dy *dy, const In *h, const float *__restrict__ weight, const In *dsum, In *dh, float *__restrict__ part,
+template <typename In, typename Dy, bool AL, int TPR, int E, bool SUM>
+__global__ __launch_bounds__((RowShape<TPR>::NT)) __attribute__((amdgpu_waves_per_eu(TPR > 256 ? 4 : 2))) void ln_bwd_kernel(
+    const Dy *dy, const In *h, const float *__restrict__ weight, const In *dsum, In *dh, float *__restrict__ partial,
     int64_t rows, int cols, float inv_n, float eps)
 {
     constexpr int RPB = RowShape<TPR>::RPB;
     __shared__ float red[TPR > 64 ? 2 * (TPR / 64) : 1];
-    const int p = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    float wv[E][V], dw[E][V], db[E][V];
+    const int grp = threadIdx.x / TPR;
+    const RowPart<TPR, AL> part = {(int)threadIdx.x % TPR, cols};
+    float wv[E][8], dw[E][8], db[E][8];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int c = (p + e * TPR) * V;
+        Pack8<float> pw;
+        part.template load<false>(pw, weight, e);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            wv[e][i] = c < cols ? weight[c + i] : 0.f;
+        for (int i = 0; i < 8; ++i) {
+            wv[e][i] = pw.get(i);
             dw[e][i] = db[e][i] = 0.f;
         }
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
         const bool live = r0 + grp < rows;
         const int64_t base = (live ? r0 + grp : rows - 1) * (int64_t)cols;
-        Pack<In, V> ph[E], pa[E];
-        Pack<Dy, V> pd[E];
+        Pack8<In> ph[E], pa[E];
+        Pack8<Dy> pd[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int c = (p + e * TPR) * V;
-            ph[e].zero();
-            pd[e].zero();
-            if (SUM) pa[e].zero();
-            if (c < cols) {
-                ph[e].load_nt(h + base + c);
-                pd[e].load_nt(dy + base + c);
-                if (SUM) pa[e].load_nt(dsum + base + c);
-            }
+            part.load(ph[e], h + base, e);
+            part.load(pd[e], dy + base, e);
+            if (SUM) part.load(pa[e], dsum + base, e);
         }
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 s[0] += ph[e].get(i);
                 s[1] += pd[e].get(i) * wv[e][i];
             }
@@ -176,54 +185,47 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_bwd_kernel(
         s[0] = s[1] = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if ((p + e * TPR) * V < cols)
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float c = ph[e].get(i) - mean;
-                    s[0] += c * c;
-                    s[1] += c * (pd[e].get(i) * wv[e][i]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float c = part.has(e, i) ? ph[e].get(i) - mean : 0.f;
+                s[0] += c * c;
+                s[1] += c * (pd[e].get(i) * wv[e][i]);
+            }
         row_sums<TPR>(s, red);
         const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
         const float gx = s[1] * rstd * inv_n;   // mean of g xh
         if (live)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int c = (p + e * TPR) * V;
-                if (c < cols) {
-                    float o[V];
+                float o[8];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float xh = (ph[e].get(i) - mean) * rstd, d = pd[e].get(i);
-                        o[i] = rstd * (d * wv[e][i] - gm - xh * gx);
-                        if (SUM) o[i] += pa[e].get(i);
-                        dw[e][i] += d * xh;
-                        db[e][i] += d;
-                    }
-                    store_row<V, true>(dh + base + c, o);
+                for (int i = 0; i < 8; ++i) {
+                    const float xh = (ph[e].get(i) - mean) * rstd, d = pd[e].get(i);
+                    o[i] = rstd * (d * wv[e][i] - gm - xh * gx);
+                    if (SUM) o[i] += pa[e].get(i);
+                    dw[e][i] += d * xh;
+                    db[e][i] += d;
                 }
+                part.store(dh + base, o, e);
             }
     }
     // the groups' sums, in group order, to this workgroup's partial row
-    float *pw = part + (size_t)blockIdx.x * 2 * cols;
+    float *pw = partial + (size_t)blockIdx.x * 2 * cols;
     if constexpr (RPB == 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int c = (p + e * TPR) * V;
-            if (c < cols) {
-                store_row<V>(pw + c, dw[e]);
-                store_row<V>(pw + cols + c, db[e]);
-            }
+            part.store(pw, dw[e], e);
+            part.store(pw + cols, db[e], e);
         }
     } else {
-        __shared__ float acc[RPB][TPR * V];
+        __shared__ float acc[RPB][TPR * 8];
 #pragma unroll
         for (int e = 0; e < 2 * E; ++e) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[grp][p * V + i] = e < E ? dw[e % E][i] : db[e % E][i];
+            for (int i = 0; i < 8; ++i) acc[grp][part.p * 8 + i] = e < E ? dw[e % E][i] : db[e % E][i];
             __syncthreads();
-            for (int c = threadIdx.x; c < TPR * V; c += RowShape<TPR>::NT) {
-                const int cc = (e % E) * TPR * V + c;
+            for (int c = threadIdx.x; c < TPR * 8; c += RowShape<TPR>::NT) {
+                const int cc = (e % E) * TPR * 8 + c;
                 if (cc < cols) {
                     float t = 0.f;
 #pragma unroll
@@ -268,7 +270,7 @@ __global__ __launch_bounds__(1024) void ln_bwd_long_kernel(
             const float xh = (in2f<In>(h[base + c]) - mean) * rstd, d = in2f<Dy>(dy[base + c]);
             float o = rstd * (d * weight[c] - gm - xh * gx);
             if (dsum) o += in2f<In>(dsum[base + c]);
-            store_row<1>(dh + base + c, &o);
+            store1(dh + base + c, o);
             pw[c] = (first ? 0.f : pw[c]) + d * xh;
             pw[cols + c] = (first ? 0.f : pw[cols + c]) + d;
         }
@@ -277,37 +279,28 @@ __global__ __launch_bounds__(1024) void ln_bwd_long_kernel(
 
 // ---- launch ------------------------------------------------------------------
 
-// Calls f with the (V, TPR, E) that holds a row of `cols` elements in
-// registers, or returns false (the long-row kernels take it). V = 8 where
-// rows keep 16-byte alignment (cols a multiple of 8).
+// Calls f with the (AL, TPR, E) that hold a row of `cols` elements in
+// registers, or returns false (the long-row kernels take it). AL: rows keep
+// 16-byte alignment. A wave a row as long as its registers hold one (2048
+// elements; 65536 x 2048 bf16 backward: 142 us, 222 with a workgroup a row).
 template <typename F> static bool for_row_shape(int cols, F f)
 {
-    auto go = [&](auto v, auto t, auto e) {
-        f(v, t, e);
+    auto go = [&](auto t, auto e) {
+        if (cols % 8 == 0) f(std::true_type{}, t, e);
+        else f(std::false_type{}, t, e);
         return true;
     };
-#define GDN2_ROW(V, T, E) \
-    if (cols <= V * T * E) \
-        return go(std::integral_constant<int, V>{}, std::integral_constant<int, T>{}, std::integral_constant<int, E>{});
-    if (cols % 8 == 0) {
-        GDN2_ROW(8, 8, 1)
-        GDN2_ROW(8, 16, 1)
-        GDN2_ROW(8, 32, 1)
-        GDN2_ROW(8, 64, 1)
-        GDN2_ROW(8, 64, 2)
-        GDN2_ROW(8, 64, 4)
-        GDN2_ROW(8, 256, 2)
-        GDN2_ROW(8, 256, 4)
-        GDN2_ROW(8, 1024, 2)
-    } else {
-        GDN2_ROW(1, 8, 1)
-        GDN2_ROW(1, 16, 1)
-        GDN2_ROW(1, 64, 1)
-        GDN2_ROW(1, 64, 4)
-        GDN2_ROW(1, 256, 4)
-        GDN2_ROW(1, 256, 16)
-        GDN2_ROW(1, 1024, 16)
-    }
+#define GDN2_ROW(T, E) \
+    if (cols <= 8 * T * E) return go(std::integral_constant<int, T>{}, std::integral_constant<int, E>{});
+    GDN2_ROW(8, 1)
+    GDN2_ROW(16, 1)
+    GDN2_ROW(32, 1)
+    GDN2_ROW(64, 1)
+    GDN2_ROW(64, 2)
+    GDN2_ROW(64, 4)
+    GDN2_ROW(256, 2)
+    GDN2_ROW(256, 4)
+    GDN2_ROW(1024, 2)
 #undef GDN2_ROW
     return false;
 }
@@ -321,11 +314,12 @@ template <typename In, typename Out> static void ln_fwd(const LayerNormArgs &a, 
         hipLaunchKernelGGL(kern, dim3(grid), dim3(nt), 0, st, (const In *)a.x, (const In *)a.residual, a.weight, a.bias,
                            (Out *)a.y, (In *)a.sum, a.rows, a.cols, inv_n, a.eps);
     };
-    const bool held = for_row_shape(a.cols, [&](auto v, auto t, auto e) {
-        constexpr int V = decltype(v)::value, T = decltype(t)::value, E = decltype(e)::value;
+    const bool held = for_row_shape(a.cols, [&](auto al, auto t, auto e) {
+        constexpr bool AL = decltype(al)::value;
+        constexpr int T = decltype(t)::value, E = decltype(e)::value;
         const int grid = ln_grid(a.rows, RowShape<T>::RPB, kLnFwdGrid);
-        if (a.residual) args(ln_fwd_kernel<In, Out, V, T, E, true>, grid, RowShape<T>::NT);
-        else args(ln_fwd_kernel<In, Out, V, T, E, false>, grid, RowShape<T>::NT);
+        if (a.residual) args(ln_fwd_kernel<In, Out, AL, T, E, true>, grid, RowShape<T>::NT);
+        else args(ln_fwd_kernel<In, Out, AL, T, E, false>, grid, RowShape<T>::NT);
     });
     if (!held) args(ln_fwd_long_kernel<In, Out>, ln_grid(a.rows, 1, kLnFwdGrid), 1024);
 }
@@ -338,10 +332,11 @@ template <typename In, typename Dy> static void ln_bwd(const LayerNormBwdArgs &a
                            (const In *)a.dsum, (In *)a.dh, (float *)a.workspace, a.rows, a.cols, inv_n, a.eps);
     };
     const int grid = ln_bwd_parts(a.rows, a.cols);
-    const bool held = for_row_shape(a.cols, [&](auto v, auto t, auto e) {
-        constexpr int V = decltype(v)::value, T = decltype(t)::value, E = decltype(e)::value;
-        if (a.dsum) args(ln_bwd_kernel<In, Dy, V, T, E, true>, grid, RowShape<T>::NT);
-        else args(ln_bwd_kernel<In, Dy, V, T, E, false>, grid, RowShape<T>::NT);
+    const bool held = for_row_shape(a.cols, [&](auto al, auto t, auto e) {
+        constexpr bool AL = decltype(al)::value;
+        constexpr int T = decltype(t)::value, E = decltype(e)::value;
+        if (a.dsum) args(ln_bwd_kernel<In, Dy, AL, T, E, true>, grid, RowShape<T>::NT);
+        else args(ln_bwd_kernel<In, Dy, AL, T, E, false>, grid, RowShape<T>::NT);
     });
     if (!held) args(ln_bwd_long_kernel<In, Dy>, grid, 1024);
 }

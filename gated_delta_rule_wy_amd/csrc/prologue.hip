@@ -244,7 +244,7 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
 #pragma unroll
                     for (int c = 0; c < V; ++c) o[c] *= r;
                 }
-                store_row<V>(y + (size_t)at * W + ch, o);
+                store8<true>(y + (size_t)at * W + ch, o, 8);
                 win[0] = win[1];
                 win[1] = win[2];
                 win[2] = cur[u];
@@ -314,7 +314,7 @@ __device__ void gate_bwd(const ProGate &gt, int64_t total, int block)
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = one(r.get(i), d.e[i]);
-        store_row<8>(dx, o);
+        store8<true>(dx, o, 8);
     } else {
         for (int i = 0; i < (int)(n - at); ++i) dx[i] = from_f<Out>(one(in2f<In>(x[i]), dy[i]));
     }

@@ -1,6 +1,6 @@
-// Row-wise helpers of the kernels around the mixer (layer norm, prologue):
-// packed loads and stores of V consecutive elements, and sums over the lanes
-// that share a row.
+// Row-wise helpers of the kernels around the mixer (layer norm, prologue, the
+// recurrence): packed loads and stores of consecutive elements, and sums over
+// the lanes that share a row.
 #pragma once
 
 #include "gdn2_device.hpp"
@@ -9,40 +9,61 @@ namespace gdn2 {
 
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
-// V consecutive elements as they lie in memory, kept packed until use (the
-// loads of a row are issued together). V = 8 needs 16-byte alignment.
-template <typename In, int V> struct Pack;
-template <> struct Pack<uint16_t, 8> {
+// Eight consecutive elements as they lie in memory, kept packed until use (the
+// loads of a row are issued together), NT: past the caches. AL: the address is a
+// multiple of 16 bytes, and all eight are there. Otherwise it is any address
+// of an element (the memory pipe takes a 16-byte load at any), and only the
+// first n are (the others are zeros).
+typedef u4 u4_any __attribute__((aligned(2)));
+typedef f4 f4_any __attribute__((aligned(4)));
+
+template <bool NT, typename T> __device__ __forceinline__ T get_as(const T *p)
+{
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+
+template <typename In> struct Pack8;
+template <> struct Pack8<uint16_t> {
     u4 r;
-    __device__ __forceinline__ void load(const uint16_t *p) { r = *reinterpret_cast<const u4 *>(p); }
-    __device__ __forceinline__ void load_nt(const uint16_t *p) { r = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p)); }
+    template <bool AL, bool NT> __device__ __forceinline__ void load(const uint16_t *p, int n)
+    {
+        if constexpr (AL) {
+            r = get_as<NT>(reinterpret_cast<const u4 *>(p));
+        } else if (n >= 8) {
+            r = get_as<NT>(reinterpret_cast<const u4_any *>(p));
+        } else {
+            zero();
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < n) r[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+        }
+    }
     __device__ __forceinline__ float get(int i) const
     {
         return __uint_as_float((i & 1) ? (r[i >> 1] & 0xFFFF0000u) : (r[i >> 1] << 16));
     }
     __device__ __forceinline__ void zero() { r = (u4){0u, 0u, 0u, 0u}; }
 };
-template <> struct Pack<float, 8> {
+template <> struct Pack8<float> {
     f4 r[2];
-    __device__ __forceinline__ void load(const float *p)
+    template <bool AL, bool NT> __device__ __forceinline__ void load(const float *p, int n)
     {
-        r[0] = reinterpret_cast<const f4 *>(p)[0];
-        r[1] = reinterpret_cast<const f4 *>(p)[1];
-    }
-    __device__ __forceinline__ void load_nt(const float *p)
-    {
-        r[0] = __builtin_nontemporal_load(reinterpret_cast<const f4 *>(p));
-        r[1] = __builtin_nontemporal_load(reinterpret_cast<const f4 *>(p) + 1);
+        if constexpr (AL) {
+            r[0] = get_as<NT>(reinterpret_cast<const f4 *>(p));
+            r[1] = get_as<NT>(reinterpret_cast<const f4 *>(p) + 1);
+        } else if (n >= 8) {
+            r[0] = get_as<NT>(reinterpret_cast<const f4_any *>(p));
+            r[1] = get_as<NT>(reinterpret_cast<const f4_any *>(p) + 1);
+        } else {
+            zero();
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < n) r[i >> 2][i & 3] = p[i];
+        }
     }
     __device__ __forceinline__ float get(int i) const { return r[i >> 2][i & 3]; }
     __device__ __forceinline__ void zero() { r[0] = r[1] = f4zero(); }
-};
-template <typename In> struct Pack<In, 1> {
-    In r;
-    __device__ __forceinline__ void load(const In *p) { r = *p; }
-    __device__ __forceinline__ void load_nt(const In *p) { r = __builtin_nontemporal_load(p); }
-    __device__ __forceinline__ float get(int) const { return in2f<In>(r); }
-    __device__ __forceinline__ void zero() { r = (In)0; }
 };
 
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
@@ -56,32 +77,41 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b)
     return __builtin_bit_cast(uint32_t, x);
 }
 
-// V floats to memory in the output type
-template <int V, bool NT = false> __device__ __forceinline__ void store_row(float *p, const float *x)
+__device__ __forceinline__ uint16_t bf16_of(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+
+// Eight floats to memory in the output type, past the caches; AL and n as in
+// Pack8::load.
+template <bool AL> __device__ __forceinline__ void store8(float *p, const float (&x)[8], int n)
 {
-    if constexpr (V == 8) {
-        f4 a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
-        if constexpr (NT) {
-            __builtin_nontemporal_store(a, reinterpret_cast<f4 *>(p));
-            __builtin_nontemporal_store(b, reinterpret_cast<f4 *>(p) + 1);
-        } else {
-            reinterpret_cast<f4 *>(p)[0] = a;
-            reinterpret_cast<f4 *>(p)[1] = b;
-        }
+    const f4 a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
+    if constexpr (AL) {
+        __builtin_nontemporal_store(a, reinterpret_cast<f4 *>(p));
+        __builtin_nontemporal_store(b, reinterpret_cast<f4 *>(p) + 1);
+    } else if (n >= 8) {
+        __builtin_nontemporal_store(a, reinterpret_cast<f4_any *>(p));
+        __builtin_nontemporal_store(b, reinterpret_cast<f4_any *>(p) + 1);
     } else {
-        *p = *x;
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < n) p[i] = x[i];
     }
 }
-template <int V, bool NT = false> __device__ __forceinline__ void store_row(uint16_t *p, const float *x)
+template <bool AL> __device__ __forceinline__ void store8(uint16_t *p, const float (&x)[8], int n)
 {
-    if constexpr (V == 8) {
-        u4 r = {bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7])};
-        if constexpr (NT) __builtin_nontemporal_store(r, reinterpret_cast<u4 *>(p));
-        else *reinterpret_cast<u4 *>(p) = r;
+    const u4 r = {bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7])};
+    if constexpr (AL) {
+        __builtin_nontemporal_store(r, reinterpret_cast<u4 *>(p));
+    } else if (n >= 8) {
+        __builtin_nontemporal_store(r, reinterpret_cast<u4_any *>(p));
     } else {
-        *p = __builtin_bit_cast(uint16_t, (__bf16)*x);
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < n) p[i] = bf16_of(x[i]);
     }
 }
+// one float
+__device__ __forceinline__ void store1(float *p, float x) { *p = x; }
+__device__ __forceinline__ void store1(uint16_t *p, float x) { *p = bf16_of(x); }
 
 // four floats to memory in the output type
 __device__ __forceinline__ void store_row4(float *p, const float *x)
