@@ -560,12 +560,18 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle: current_stream() builds a Stream object around
+# it, most of the host's time of a small call (1.9 of 12 us).
+_raw_stream = getattr(torch._C, '_cuda_getCurrentRawStream', None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, where: str, dev: torch.device, *args) -> None:
     """Call the library on ``dev``'s current stream, with ``dev`` current."""
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
             return _call(fn, where, dev, *args)
-    _lib.gdn2_set_stream(torch.cuda.current_stream(dev).cuda_stream)
+    _lib.gdn2_set_stream(_raw_stream(dev.index))
     st = fn(*args)
     if st != GDN2_OK:
         raise Gdn2Error(st, where)
@@ -648,28 +654,31 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: 
 
 def _conv_pools(conv_weight, conv_bias, conv_state, conv_state_out, heads, dims, dt, dev):
     """ShortConv of a prologue call whose histories are pools, and their slots."""
-    sc = ShortConv()
     if conv_weight is None or len(conv_weight) != 3:
         raise ValueError('conv_weight must be a (q, k, v) triple of [heads*d, 4] float32 tensors')
-    slots = 0
-    for n, t, h, d in zip('qkv', conv_weight, heads, dims):
-        _need(t, f'conv_weight[{n}]', (h * d, 4), torch.float32, dev)
-        setattr(sc, f'weight_{n}', t.data_ptr())
+    addr = [None] * 12   # the struct's fields in order
+    slots, f32 = 0, torch.float32
+    for z, (t, h, d) in enumerate(zip(conv_weight, heads, dims)):
+        _need(t, 'conv_weight', (h * d, 4), f32, dev)
+        addr[z] = t.data_ptr()
     if conv_bias is not None:
-        for n, t, h, d in zip('qkv', conv_bias, heads, dims):
+        for z, (t, h, d) in enumerate(zip(conv_bias, heads, dims)):
             if t is not None:
-                _need(t, f'conv_bias[{n}]', (h * d,), torch.float32, dev)
-                setattr(sc, f'bias_{n}', t.data_ptr())
-    for label, trip in (('in', conv_state), ('out', conv_state_out)):
+                _need(t, 'conv_bias', (h * d,), f32, dev)
+                addr[3 + z] = t.data_ptr()
+    for at, trip in ((6, conv_state), (9, conv_state_out)):
         if trip is None:
             continue
         if len(trip) != 3:
             raise ValueError('conv_state must be a (q, k, v) triple')
-        for n, t, h, d in zip('qkv', trip, heads, dims):
+        if at == 9 and trip is conv_state:
+            addr[9:] = addr[6:9]
+            continue
+        for z, (t, h, d) in enumerate(zip(trip, heads, dims)):
             slots = slots or t.shape[0]
-            _need(t, f'conv_state_{label}[{n}]', (slots, h, 3, d), dt, dev)
-            setattr(sc, f'state_{label}_{n}', t.data_ptr())
-    return sc, slots
+            _need(t, 'conv_state', (slots, h, 3, d), dt, dev)
+            addr[at + z] = t.data_ptr()
+    return ShortConv(*addr), slots
 
 
 def _prologue_sizes(q_raw, k_raw, v_raw, b_logit, w_logit, cu_seqlens):
@@ -737,13 +746,16 @@ def prologue_bwd(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor, 
     grad_dtype = dt if grad_dtype is None else grad_dtype
     if grad_dtype not in _CODES:
         raise TypeError(f'unsupported gradient dtype {grad_dtype} (bfloat16 or float32)')
-    g = {n: torch.empty(x.shape, dtype=grad_dtype, device=dev)
-         for n, x in zip(('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit'), raw)}
-    for n, h, d in zip('qkv', heads, dims):
-        g['weight_' + n] = torch.empty((h * d, 4), dtype=torch.float32, device=dev)
-    for z, (n, h, d) in enumerate(zip('qkv', heads, dims)):
-        if conv_bias is not None and conv_bias[z] is not None:
-            g['bias_' + n] = torch.empty((h * d,), dtype=torch.float32, device=dev)
+    like = raw if grad_dtype is dt else grads if grad_dtype is torch.float32 else None
+    if like is None:
+        like = [torch.empty(x.shape, dtype=grad_dtype, device=dev) for x in raw]
+    g = {n: torch.empty_like(x) for n, x in zip(('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit'), like)}
+    for n, x in zip('qkv', conv_weight):
+        g['weight_' + n] = torch.empty_like(x)
+    if conv_bias is not None:
+        for n, x in zip('qkv', conv_bias):
+            if x is not None:
+                g['bias_' + n] = torch.empty_like(x)
     need = _lib.gdn2_prologue_bwd_workspace_bytes(B, T, N, H, HK, Dk, Dv, int(cu_seqlens is not None))
     if need == 0:
         raise Gdn2Error(GDN2_ERR_UNSUPPORTED, 'gdn2_prologue_bwd_workspace_bytes')
@@ -788,7 +800,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     if out_dtype not in _CODES:
         raise TypeError(f'unsupported output dtype {out_dtype} (bfloat16 or float32)')
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = torch.empty_like(x) if out_dtype is dt else torch.empty(shape, dtype=out_dtype, device=dev)
     else:
         _need(out, 'out', shape, out_dtype, dev)
     _call(_lib.gdn2_layer_norm_fwd, 'gdn2_layer_norm_fwd', dev, x.data_ptr(), _addr(residual), weight.data_ptr(),

@@ -10,10 +10,13 @@
 //     dlogit = dgate s (1 - s)
 //
 // Bound by memory: every element is read once and written once. A thread owns
-// V neighbouring channels of one tensor (16 bytes of bf16; the lanes of a head
-// are neighbours, and its norm a sum over them) and walks along the tokens
-// with the last three inputs in registers, four rows of loads ahead. All sums
-// are fp32; outputs are rounded once.
+// a few neighbouring channels of one tensor (the lanes of a head are
+// neighbours, and its norm a sum over them) and walks along the tokens with the
+// last three inputs in registers, eight rows of loads ahead. Few channels a
+// thread, so that many waves fit: forward over 32 packed sequences of up to
+// 2048 tokens, 16 heads of 128, bf16: 274 us with four (5.4 TB/s), 296 with
+// eight; backward over 8 of up to 4096: 367 us with two (5.5 TB/s), 379 with
+// four. All sums are fp32; outputs are rounded once.
 #include "gdn2_launch.hpp"
 #include "rows.hpp"
 
@@ -22,16 +25,29 @@
 namespace gdn2 {
 
 constexpr int kNT = 256;
+constexpr int kFwdV = 4, kBwdV = 2;   // channels of a thread
 
-// Sum over aligned groups of G lanes, G a power of two up to 32, in each of
-// them; the group's lanes are active together.
+// Sum over aligned groups of G lanes (a power of two up to 64), in each of
+// them: swaps within rows of 16 lanes, each adding the halves that hold their
+// sums, and gfx950's swaps of rows beyond. All lanes of a group are active
+// together; G is the same for the workgroup.
 __device__ __forceinline__ float head_sum(float x, int G)
 {
-    if (G >= 2) x += __shfl_xor(x, 1);
-    if (G >= 4) x += __shfl_xor(x, 2);
-    if (G >= 8) x += __shfl_xor(x, 4);
-    if (G >= 16) x += __shfl_xor(x, 8);
-    if (G >= 32) x += __shfl_xor(x, 16);
+    auto add = [](float v, auto ctrl) {
+        return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    x = add(x, std::integral_constant<int, 0xB1>{});                  // quad_perm [1,0,3,2]
+    if (G >= 4) x = add(x, std::integral_constant<int, 0x4E>{});      // quad_perm [2,3,0,1]
+    if (G >= 8) x = add(x, std::integral_constant<int, 0x141>{});     // row_half_mirror
+    if (G >= 16) x = add(x, std::integral_constant<int, 0x140>{});    // row_mirror
+    if (G >= 32) {
+        const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
+    if (G >= 64) {
+        const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
     return x;
 }
 
@@ -69,7 +85,8 @@ template <typename In, int V> struct PackV {
     __device__ __forceinline__ void load(const In *p)
     {
         constexpr int B = V * sizeof(In);
-        if constexpr (B == 8) *reinterpret_cast<uint2 *>(e) = *reinterpret_cast<const uint2 *>(p);
+        if constexpr (B == 4) *reinterpret_cast<uint32_t *>(e) = *reinterpret_cast<const uint32_t *>(p);
+        else if constexpr (B == 8) *reinterpret_cast<uint2 *>(e) = *reinterpret_cast<const uint2 *>(p);
         else
 #pragma unroll
             for (int i = 0; i < B / 16; ++i) reinterpret_cast<u4 *>(e)[i] = reinterpret_cast<const u4 *>(p)[i];
@@ -77,7 +94,8 @@ template <typename In, int V> struct PackV {
     __device__ __forceinline__ void store(In *p) const
     {
         constexpr int B = V * sizeof(In);
-        if constexpr (B == 8) *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(e);
+        if constexpr (B == 4) *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(e);
+        else if constexpr (B == 8) *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(e);
         else
 #pragma unroll
             for (int i = 0; i < B / 16; ++i) reinterpret_cast<u4 *>(p)[i] = reinterpret_cast<const u4 *>(e)[i];
@@ -103,7 +121,10 @@ struct ProTensor {
     void *hout;
     void *y;
     int heads, d;        // channels a token: heads * d
-    int block0, blocks;  // its workgroups
+    int ld;              // log2 d
+    // its workgroups: `per` of them pass over a tile's vectors of channels, or
+    // (per = 0) one over `rows` tiles
+    int block0, blocks, per, rows;
 };
 struct ProGate {
     const void *x;
@@ -120,6 +141,23 @@ struct ProParams {
     int slots, tile;     // tokens a thread walks over
 };
 
+// This thread's tile and first channel, V of them: false where it has none
+// (a head's lanes always agree).
+template <int V> __device__ __forceinline__ bool my_part(const ProTensor &t, int block, int64_t &tile, int &ch)
+{
+    const int nvec = t.heads * t.d / V;
+    if (t.per > 0) {
+        const int v = block % t.per * kNT + threadIdx.x;
+        tile = block / t.per;
+        ch = v * V;
+        return v < nvec;
+    }
+    const int r = threadIdx.x / (unsigned)nvec;
+    tile = (int64_t)block * t.rows + r;
+    ch = (threadIdx.x - r * nvec) * V;
+    return r < t.rows;
+}
+
 // History element j (0..2, oldest first) of sequence i for the V channels at
 // ch (head ch / d), or zeros.
 template <typename In, int V>
@@ -127,7 +165,7 @@ __device__ __forceinline__ void load_history(PackV<In, V> &r, const ProTensor &t
 {
     const int slot = p.slot_in ? p.slot_in[i] : i;
     if (t.hin && (unsigned)slot < (unsigned)p.slots)
-        r.load((const In *)t.hin + (((size_t)slot * t.heads + ch / t.d) * 3 + j) * t.d + ch % t.d);
+        r.load((const In *)t.hin + ((((size_t)slot * t.heads + (ch >> t.ld)) * 3 + j) << t.ld) + (ch & (t.d - 1)));
     else r.zero();
 }
 
@@ -155,15 +193,16 @@ __device__ void gate_fwd(const ProGate &gt, int64_t total, int block)
     if (at >= n) return;
     const In *x = (const In *)gt.x + at;
     In *y = (In *)gt.y + at;
-    auto one = [](float z) { return from_f<In>(__builtin_amdgcn_rcpf(1.f + __expf(-z))); };
+    auto one = [](float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); };
     if (at + 8 <= n) {
         PackV<In, 8> r;
         r.load(x);
+        float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r.e[i] = one(r.get(i));
-        r.store(y);
+        for (int i = 0; i < 8; ++i) o[i] = one(r.get(i));
+        store8<true>(y, o, 8);
     } else {
-        for (int i = 0; i < (int)(n - at); ++i) y[i] = one(in2f<In>(x[i]));
+        for (int i = 0; i < (int)(n - at); ++i) y[i] = from_f<In>(one(in2f<In>(x[i])));
     }
 }
 
@@ -172,7 +211,7 @@ __device__ void gate_fwd(const ProGate &gt, int64_t total, int block)
 template <typename In, bool OWN>
 __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
 {
-    constexpr int V = 8, U = 4;
+    constexpr int V = kFwdV, U = OWN ? 4 : 8;   // U: rows of loads ahead
     const int total = p.sq.total();
     const int bid = blockIdx.x;
 #pragma unroll
@@ -184,10 +223,10 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
     const int z = bid >= p.t[2].block0 ? 2 : (bid >= p.t[1].block0 ? 1 : 0);
     const ProTensor &t = p.t[z];
     const size_t W = (size_t)t.heads * t.d;
-    const int nvec = (int)(W / V), G = t.d / V;
-    const int64_t id = (int64_t)(bid - t.block0) * kNT + threadIdx.x;
-    const int64_t tl = id / nvec;
-    const int ch = (int)(id % nvec) * V;
+    const int G = t.d / V;
+    int64_t tl;
+    int ch;
+    if (!my_part<V>(t, bid - t.block0, tl, ch)) return;
     int i, tb, te;
     if (OWN) {
         if (tl >= p.sq.N) return;   // (a head's lanes leave together)
@@ -210,8 +249,16 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
         bias[c] = t.bias ? t.bias[ch + c] : 0.f;
     }
     PackV<In, V> win[3];
+    float old[3][V];   // win as numbers
+    auto numbers = [&]() {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+            for (int c = 0; c < V; ++c) old[j][c] = win[j].get(c);
+    };
     int s0 = p.sq.start(i), s1 = p.sq.end(i);
     load_window<In, V>(win, t, p, i, s0, tb - s0 - 3, ch);
+    numbers();
     PackV<In, V> nxt[U];
     if (tb < te)
 #pragma unroll
@@ -231,23 +278,33 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
                     s0 = p.sq.start(i);
                     s1 = p.sq.end(i);
                     load_window<In, V>(win, t, p, i, s0, -3, ch);
+                    numbers();
                 }
                 float o[V], ss = 0.f;
 #pragma unroll
                 for (int c = 0; c < V; ++c) {
-                    o[c] = bias[c] + tap[c][0] * win[0].get(c) + tap[c][1] * win[1].get(c) + tap[c][2] * win[2].get(c) +
-                           tap[c][3] * cur[u].get(c);
+                    const float now = cur[u].get(c);
+                    o[c] = bias[c] + tap[c][0] * old[0][c] + tap[c][1] * old[1][c] + tap[c][2] * old[2][c] +
+                           tap[c][3] * now;
                     ss += o[c] * o[c];
+                    old[0][c] = old[1][c];
+                    old[1][c] = old[2][c];
+                    old[2][c] = now;
                 }
                 if (z < 2) {
                     const float r = rsqrtf(fmaxf(head_sum(ss, G), 1e-24f));
 #pragma unroll
                     for (int c = 0; c < V; ++c) o[c] *= r;
                 }
-                store8<true>(y + (size_t)at * W + ch, o, 8);
-                win[0] = win[1];
-                win[1] = win[2];
-                win[2] = cur[u];
+                PackV<In, V> out;
+#pragma unroll
+                for (int c = 0; c < V; ++c) out.e[c] = from_f<In>(o[c]);
+                out.store(y + (size_t)at * W + ch);
+                if (OWN) {
+                    win[0] = win[1];
+                    win[1] = win[2];
+                    win[2] = cur[u];
+                }
             }
         }
     }
@@ -255,11 +312,11 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
         const int slot = p.slot_out ? p.slot_out[i] : (p.slot_in ? p.slot_in[i] : i);
         if ((unsigned)slot >= (unsigned)p.slots) return;
         const int keep = p.commit ? min(max(p.commit[i], 0), te - tb) : te - tb;
-        PackV<In, V> h[3];
-        load_window<In, V>(h, t, p, i, tb, keep - 3, ch);
+        // (win holds the last three inputs, or the old history's)
+        if (keep < te - tb) load_window<In, V>(win, t, p, i, tb, keep - 3, ch);
 #pragma unroll
         for (int j = 0; j < 3; ++j)
-            h[j].store((In *)t.hout + (((size_t)slot * t.heads + ch / t.d) * 3 + j) * t.d + ch % t.d);
+            win[j].store((In *)t.hout + ((((size_t)slot * t.heads + (ch >> t.ld)) * 3 + j) << t.ld) + (ch & (t.d - 1)));
     }
 }
 
@@ -268,12 +325,12 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
 template <typename In> __global__ __launch_bounds__(kNT) void prologue_history_kernel(ProParams p)
 {
     constexpr int V = 8;
-    const ProTensor &t = p.t[blockIdx.y];
-    const int nvec = t.heads * t.d / V;
-    const int64_t id = (int64_t)blockIdx.x * kNT + threadIdx.x;
-    const int64_t tl = id / nvec;
-    if (tl >= p.sq.N) return;
-    const int i = (int)tl, ch = (int)(id % nvec) * V;
+    const int bid = blockIdx.x;
+    const ProTensor &t = p.t[bid >= p.t[2].block0 ? 2 : (bid >= p.t[1].block0 ? 1 : 0)];
+    int64_t tl;
+    int ch;
+    if (!my_part<V>(t, bid - t.block0, tl, ch) || tl >= p.sq.N) return;
+    const int i = (int)tl;
     const int slot = p.slot_out ? p.slot_out[i] : (p.slot_in ? p.slot_in[i] : i);
     if ((unsigned)slot >= (unsigned)p.slots) return;
     const int tb = p.sq.start(i), len = p.sq.end(i) - tb;
@@ -282,7 +339,7 @@ template <typename In> __global__ __launch_bounds__(kNT) void prologue_history_k
     load_window<In, V>(h, t, p, i, tb, keep - 3, ch);
 #pragma unroll
     for (int j = 0; j < 3; ++j)
-        h[j].store((In *)t.hout + (((size_t)slot * t.heads + ch / t.d) * 3 + j) * t.d + ch % t.d);
+        h[j].store((In *)t.hout + ((((size_t)slot * t.heads + (ch >> t.ld)) * 3 + j) << t.ld) + (ch & (t.d - 1)));
 }
 
 // ---- backward ------------------------------------------------------------------
@@ -323,7 +380,7 @@ __device__ void gate_bwd(const ProGate &gt, int64_t total, int block)
 template <typename In, typename Out>
 __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
 {
-    constexpr int V = 4, U = 4;
+    constexpr int V = kBwdV, U = 8;
     const int total = p.f.sq.total();
     const int bid = blockIdx.x;
 #pragma unroll
@@ -335,10 +392,10 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
     const int z = bid >= p.f.t[2].block0 ? 2 : (bid >= p.f.t[1].block0 ? 1 : 0);
     const ProTensor &t = p.f.t[z];
     const size_t W = (size_t)t.heads * t.d;
-    const int nvec = (int)(W / V), G = t.d / V;
-    const int64_t id = (int64_t)(bid - t.block0) * kNT + threadIdx.x;
-    const int64_t tl = id / nvec;
-    const int ch = (int)(id % nvec) * V;
+    const int G = t.d / V;
+    int64_t tl;
+    int ch;
+    if (!my_part<V>(t, bid - t.block0, tl, ch)) return;
     // every tile up to the last token the sizes allow has its partial row;
     // those behind the last sequence write zeros
     if (tl * p.f.tile >= (p.f.sq.cu ? (int64_t)p.f.sq.T : (int64_t)p.f.sq.N * p.f.sq.T)) return;
@@ -363,8 +420,16 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
             a[0][c] = a[1][c] = a[2][c] = 0.f;
         }
         int i = p.f.sq.of(tb), s0 = p.f.sq.start(i), s1 = p.f.sq.end(i);
-        PackV<In, V> win[3];
-        load_window<In, V>(win, t, p.f, i, s0, tb - s0 - 3, ch);
+        float old[3][V];   // the three inputs before a token
+        auto window = [&](int pos) {
+            PackV<In, V> win[3];
+            load_window<In, V>(win, t, p.f, i, s0, pos, ch);
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+#pragma unroll
+                for (int c = 0; c < V; ++c) old[j][c] = win[j].get(c);
+        };
+        window(tb - s0 - 3);
         // up to three tokens past the tile, of the sequence of its last one
         const int il = p.f.sq.of(te - 1);
         const int th = max(te, min(te + 3, p.f.sq.end(il)));
@@ -396,17 +461,20 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
                         i = p.f.sq.next(i, at);
                         s0 = p.f.sq.start(i);
                         s1 = p.f.sq.end(i);
-                        load_window<In, V>(win, t, p.f, i, s0, -3, ch);
+                        window(-3);
                     }
-                    float d[V];
+                    float d[V], now[V];
 #pragma unroll
-                    for (int c = 0; c < V; ++c) d[c] = cd[u].e[c];
+                    for (int c = 0; c < V; ++c) {
+                        d[c] = cd[u].e[c];
+                        now[c] = cx[u].get(c);
+                    }
                     if (z < 2) {
                         float y[V], ss = 0.f, yd = 0.f;
 #pragma unroll
                         for (int c = 0; c < V; ++c) {
-                            y[c] = bias[c] + tap[c][0] * win[0].get(c) + tap[c][1] * win[1].get(c) +
-                                   tap[c][2] * win[2].get(c) + tap[c][3] * cx[u].get(c);
+                            y[c] = bias[c] + tap[c][0] * old[0][c] + tap[c][1] * old[1][c] + tap[c][2] * old[2][c] +
+                                   tap[c][3] * now[c];
                             ss += y[c] * y[c];
                             yd += y[c] * d[c];
                         }
@@ -421,10 +489,10 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
                     if (at < te) {
 #pragma unroll
                         for (int c = 0; c < V; ++c) {
-                            dw[c][0] += d[c] * win[0].get(c);
-                            dw[c][1] += d[c] * win[1].get(c);
-                            dw[c][2] += d[c] * win[2].get(c);
-                            dw[c][3] += d[c] * cx[u].get(c);
+                            dw[c][0] += d[c] * old[0][c];
+                            dw[c][1] += d[c] * old[1][c];
+                            dw[c][2] += d[c] * old[2][c];
+                            dw[c][3] += d[c] * now[c];
                             db[c] += d[c];
                         }
                     }
@@ -439,7 +507,12 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
                     }
                     const int low = max(tb, s0);
                     auto put = [&](int to, const float *v) {
-                        if (to >= low && to < te) store_row4(dx + (size_t)to * W + ch, v);
+                        if (to >= low && to < te) {
+                            PackV<Out, V> r;
+#pragma unroll
+                            for (int c = 0; c < V; ++c) r.e[c] = from_f<Out>(v[c]);
+                            r.store(dx + (size_t)to * W + ch);
+                        }
                     };
                     put(at - 3, o);
                     if (at == s1 - 1) {   // the sequence's last token: nothing follows
@@ -449,9 +522,12 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
 #pragma unroll
                         for (int c = 0; c < V; ++c) a[0][c] = a[1][c] = a[2][c] = 0.f;
                     }
-                    win[0] = win[1];
-                    win[1] = win[2];
-                    win[2] = cx[u];
+#pragma unroll
+                    for (int c = 0; c < V; ++c) {
+                        old[0][c] = old[1][c];
+                        old[1][c] = old[2][c];
+                        old[2][c] = now[c];
+                    }
                 }
             }
         }
@@ -459,8 +535,10 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
     float *part = p.part[z] + (size_t)tl * 5 * W;
 #pragma unroll
     for (int c = 0; c < V; ++c) *reinterpret_cast<f4 *>(part + 4 * (size_t)(ch + c)) = dw[c];
-    f4 b4 = {db[0], db[1], db[2], db[3]};
-    *reinterpret_cast<f4 *>(part + 4 * W + ch) = b4;
+    PackV<float, V> b;
+#pragma unroll
+    for (int c = 0; c < V; ++c) b.e[c] = db[c];
+    b.store(part + 4 * W + ch);
 }
 
 // ---- launch --------------------------------------------------------------------
@@ -481,8 +559,12 @@ static ProParams pro_params(const PrologueArgs &a, int V, int64_t tiles, int til
         t.y = a.y[z];
         t.heads = a.heads[z];
         t.d = a.d[z];
+        t.ld = __builtin_ctz(t.d);
+        const int nvec = t.heads * t.d / V;
+        t.per = nvec >= kNT ? (nvec + kNT - 1) / kNT : 0;
+        t.rows = nvec >= kNT ? 0 : kNT / nvec;
         t.block0 = at;
-        t.blocks = (int)((tiles * (t.heads * t.d / V) + kNT - 1) / kNT);
+        t.blocks = (int)(t.per ? tiles * t.per : (tiles + t.rows - 1) / t.rows);
         at += t.blocks;
     }
     for (int z = 0; z < 2; ++z) {
@@ -512,9 +594,9 @@ template <typename In> static hipError_t prologue_fwd_t(const PrologueArgs &a, h
 {
     const bool own = a.T <= kOwnTokens, hist = a.hist_out[0] != nullptr;
     const int64_t tokens = tokens_of(a);
-    const int tile = 32;
+    const int tile = 64;
     int blocks = 0;
-    const ProParams p = pro_params(a, 8, own ? a.N : (tokens + tile - 1) / tile, tile, &blocks);
+    const ProParams p = pro_params(a, kFwdV, own ? a.N : (tokens + tile - 1) / tile, tile, &blocks);
     if (blocks > 0 && (tokens > 0 || (own && hist))) {
         prof_before("gdn2_prologue_fwd", st);
         if (own) hipLaunchKernelGGL((prologue_fwd_kernel<In, true>), dim3(blocks), dim3(kNT), 0, st, p);
@@ -524,11 +606,10 @@ template <typename In> static hipError_t prologue_fwd_t(const PrologueArgs &a, h
         if (err != hipSuccess) return err;
     }
     if (own || !hist) return hipSuccess;
-    int widest = 0;
-    for (int z = 0; z < 3; ++z) widest = std::max(widest, a.heads[z] * a.d[z]);
+    int hblocks = 0;
+    ProParams h = pro_params(a, 8, a.N, 0, &hblocks);
     prof_before("gdn2_prologue_history", st);
-    hipLaunchKernelGGL((prologue_history_kernel<In>), dim3((unsigned)(((int64_t)a.N * (widest / 8) + kNT - 1) / kNT), 3),
-                       dim3(kNT), 0, st, p);
+    hipLaunchKernelGGL((prologue_history_kernel<In>), dim3(h.g[0].block0), dim3(kNT), 0, st, h);
     prof_after(st);
     return hipGetLastError();
 }
@@ -538,12 +619,12 @@ hipError_t launch_prologue_fwd(const PrologueArgs &a, hipStream_t st)
     return a.bf16 ? prologue_fwd_t<uint16_t>(a, st) : prologue_fwd_t<float>(a, st);
 }
 
-// Tokens a backward thread walks over (four channels each): enough threads to
+// Tokens a backward thread walks over: enough threads to
 // fill the chip twice over (256 CUs x 8 waves), between 16 and 256 tokens (a
 // tile reads three rows before and three after its own).
 int prologue_bwd_tile(long long tokens, long long channels)
 {
-    const long long t = tokens * (channels / 4) / (256LL * 8 * 64);
+    const long long t = tokens * (channels / kBwdV) / (256LL * 8 * 64);
     return (int)std::max(16LL, std::min(256LL, (t + 3) / 4 * 4));
 }
 
@@ -562,7 +643,7 @@ template <typename In, typename Out> static hipError_t prologue_bwd_t(const Prol
     const int64_t tiles = (tokens + tile - 1) / tile;
     int blocks = 0;
     ProBwdParams p = {};
-    p.f = pro_params(a.f, 4, tiles, tile, &blocks);
+    p.f = pro_params(a.f, kBwdV, tiles, tile, &blocks);
     float *part = (float *)a.workspace;
     ColumnSums cs = {};
     for (int z = 0; z < 3; ++z) {

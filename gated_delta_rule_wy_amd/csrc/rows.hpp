@@ -113,17 +113,6 @@ template <bool AL> __device__ __forceinline__ void store8(uint16_t *p, const flo
 __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store1(uint16_t *p, float x) { *p = bf16_of(x); }
 
-// four floats to memory in the output type
-__device__ __forceinline__ void store_row4(float *p, const float *x)
-{
-    f4 a = {x[0], x[1], x[2], x[3]};
-    *reinterpret_cast<f4 *>(p) = a;
-}
-__device__ __forceinline__ void store_row4(uint16_t *p, const float *x)
-{
-    *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
-}
-
 // Sum over the TPR threads that share a row, in each of them: TPR <= 64 lanes
 // of a wave, or all TPR threads of a workgroup through `red` (TPR / 64 floats
 // per value, and a barrier pair). Every thread of the workgroup calls it.
