@@ -13,8 +13,9 @@
 //   Delta = X (U - R_E),  O = R_Q + P Delta
 //   S = D_8 S0 + (k alpha_{t+1} .. alpha_8)^T Delta
 // Decays are running products of alphas, so log alpha may be anything down to
-// -inf (a full forget); the quotients need D_s >= 2^-100, and a block with
-// less is cut in half, down to a single token, which has none. All of it is
+// -inf (a full forget); the quotients need D_s >= 2^-60 (the
+// products then stay far from the smallest floats), and a block with less is
+// cut in half, down to a single token, which has none. All of it is
 // fp32, the products on the fp32 matrix instruction.
 //
 // A workgroup of dv/16 waves owns the state of one (sequence, head), a wave 16
@@ -27,6 +28,14 @@
 // third one (by the decayed keys) takes it. The state thus never moves between
 // lanes and is read and written once however many tokens follow, which is what
 // the operator is bound by: 8 bytes a state element.
+//
+// Measured at 128 x 128 heads (bf16 inputs): 256 sequences x 16 heads, one
+// token, 110 us (4.9 TB/s; the same bytes multiplied in place by a library
+// kernel 91 us); 128 sequences x 32 heads of 0 to 8 tokens, part committed,
+// 89 us (5.4 TB/s). With more tokens a sequence the blocks come one after the
+// other: about 2.7 us a block of one chain alone, of which the products are 1800
+// cycles of 6300; 48 sequences x 16 heads of up to 64 fp32 tokens (128 x 64)
+// take 43 us, a third of them at the matrix cores' rate.
 #pragma once
 
 #include "gdn2_launch.hpp"
@@ -246,7 +255,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
     //  - a token holds a NaN or an infinity: the products multiply what comes
     //    after a token by zeros, which hides any other number. First without a
     //    draft's end (its committed part stays one block), then token by token;
-    //  - a channel decays by more than 2^100 within it: A and P are formed as
+    //  - a channel decays by more than 2^60 within it: A and P are formed as
     //    products of rows decayed from the block's start and keys divided by
     //    that decay. Half the tokens, down to one, which needs neither.
     int most = C, L = 0, par = 0;
@@ -326,7 +335,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
             }
             scan(dd, up, on, all, lane);
             f4 ki;
-            wide = wide || !(fminf(fminf(up[0], up[1]), fminf(up[2], up[3])) >= 0x1p-100f);
+            wide = wide || !(fminf(fminf(up[0], up[1]), fminf(up[2], up[3])) >= 0x1p-60f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 ki[e] = L > 1 ? kk[e] * __builtin_amdgcn_rcpf(up[e]) : kk[e];
