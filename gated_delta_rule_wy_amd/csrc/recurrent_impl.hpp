@@ -18,8 +18,8 @@
 // cut in half, down to a single token, which has none. All of it is
 // fp32, the products on the fp32 matrix instruction.
 //
-// A workgroup of dv/16 waves owns the state of one (sequence, head), a wave 16
-// columns of it in registers: tile r, lane n + 16g holds rows 16r + 4g + j of
+// A workgroup of dv/16 waves (or half as many) owns the state of one (sequence,
+// head), or half its columns, a wave 16 of them in registers: tile r, lane n + 16g holds rows 16r + 4g + j of
 // column n, which is the accumulator layout, and with element j of a 16-deep
 // fragment on row 4g + j also the right operand's. The block's 16 left rows are
 // ordered so that rows 4g .. 4g+3 are the erase rows of tokens g and g+4 and
@@ -82,10 +82,10 @@ template <> struct Raw4<float> {
     __device__ __forceinline__ f4 get() const { return r; }
 };
 
-template <typename In, int DK, int NW>
+template <typename In, int DK, int DV, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 ? 3 : 4))) void recurrent_kernel(RecParams a)
 {
-    constexpr int C = kRecTokens, NT = 64 * NW, NR = DK / 16, DV = 16 * NW;
+    constexpr int C = kRecTokens, NT = 64 * NW, NR = DK / 16, WGC = DV / (16 * NW);   // WGC: workgroups of a chain
     constexpr int XS = DK + 4;    // row stride of the fragment tiles (16-byte rows)
     // A lane takes four channels of a token, a wave 8 tokens of 32 channels
     constexpr int C4 = DK / 4, NCH = (DK + 31) / 32, IPT = (NCH + NW - 1) / NW;
@@ -94,11 +94,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
     __shared__ float sM[16][C + 1];
     __shared__ int2 sFlag[2];   // of even and odd blocks: x: a value is not finite, y: a wide decay
 
-    const int i = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const int chain = blockIdx.x / WGC, i = chain / a.H, h = chain % a.H;
+    const int col0 = blockIdx.x % WGC * 16 * NW;
     const int hk = h / (a.H / a.HK);
     const int tid = threadIdx.x, lane = tid & 63, wv = wave_id();
     const int n = lane & 15, g = lane >> 4;
-    const int col = 16 * wv + n;
+    const int col = col0 + 16 * wv + n;
 
     int t0, t1;
     if (a.cu) {
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
             if (NCH % NW == 0 || wv + m * NW < NCH) load_item(tb, min(lane >> 3, L - 1), DK < 32 ? c % DK : c, x[m]);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) load_u(tb, min((lane >> 4) + 4 * j, L - 1), 16 * wv + (lane & 15), cu[j]);
+        for (int j = 0; j < 2; ++j) load_u(tb, min((lane >> 4) + 4 * j, L - 1), col0 + 16 * wv + (lane & 15), cu[j]);
     };
     // Of the products of d over a channel's 8 tokens (lanes 8 apart): up to the
     // lane's token, behind it, and of all. Each step joins the groups of
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
         // (the lane's addresses are formed anew in each block: kept over the
         // loop they would take a third of the registers)
         asm volatile("" : "+v"(lane));
-        const int n = lane & 15, g = lane >> 4, col = 16 * wv + n;
+        const int n = lane & 15, g = lane >> 4, col = col0 + 16 * wv + n;
         const int tb = t0 + done;
         // ---- the block's rows; tokens past it are zeros that decay nothing
         // (those whose effect stays: all but those of a draft's end)
@@ -457,21 +458,33 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 
     }
 }
 
-template <typename In, int DK, int NW> static void rec_go(const RecurrentArgs &a, hipStream_t st)
+template <typename In, int DK, int DV, int NW> static void rec_go(const RecurrentArgs &a, hipStream_t st)
 {
     RecParams p = {a.q, a.k, a.v, a.b, a.w, a.log_alpha, a.state, a.slot_in, a.slot_out, a.commit, a.cu_seqlens, a.o,
                    a.T, a.H, a.HK, a.slots, a.gates, a.out_bf16};
-    hipLaunchKernelGGL((recurrent_kernel<In, DK, NW>), dim3(a.N * a.H), dim3(64 * NW), 0, st, p);
+    hipLaunchKernelGGL((recurrent_kernel<In, DK, DV, NW>), dim3(a.N * a.H * (DV / (16 * NW))), dim3(64 * NW), 0, st, p);
+}
+
+// A workgroup a chain, unless two workgroups a chain still leave every compute
+// unit at most one: then a chain of eight waves is cut in two, so that each
+// wave has a matrix core to itself (one chain, 64 tokens, 128 x 128: 34 -> 28
+// us; 128 chains: 37 -> 33; 256 chains: 41 either way; 256 x 16 chains of one
+// token: 111 us whole, 113 in two, 126 in four).
+template <typename In, int DK, int DV> static void rec_split(const RecurrentArgs &a, hipStream_t st)
+{
+    constexpr int ALL = DV / 16, CUS = 256;
+    if (ALL > 4 && (long long)a.N * a.H * 2 <= CUS) rec_go<In, DK, DV, (ALL < 4 ? ALL : 4)>(a, st);
+    else rec_go<In, DK, DV, ALL>(a, st);
 }
 
 template <typename In, int DK> static hipError_t rec_dv(const RecurrentArgs &a, hipStream_t st)
 {
     prof_before("gdn2_recurrent", st);
     switch (a.dv) {
-    case 16: rec_go<In, DK, 1>(a, st); break;
-    case 32: rec_go<In, DK, 2>(a, st); break;
-    case 64: rec_go<In, DK, 4>(a, st); break;
-    case 128: rec_go<In, DK, 8>(a, st); break;
+    case 16: rec_split<In, DK, 16>(a, st); break;
+    case 32: rec_split<In, DK, 32>(a, st); break;
+    case 64: rec_split<In, DK, 64>(a, st); break;
+    case 128: rec_split<In, DK, 128>(a, st); break;
     default: return hipErrorInvalidValue;
     }
     prof_after(st);
