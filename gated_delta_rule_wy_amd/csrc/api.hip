@@ -645,7 +645,7 @@ int gdn2_layer_norm_fwd(const void *x, const void *residual, const float *weight
 {
     const int st = layer_norm_check(rows, cols, eps, in_dtype, out_dtype);
     if (st != GDN2_OK) return st;
-    if (rows > 0 && (!x || !weight || !y)) return GDN2_ERR_INVALID;
+    if (rows > 0 && (!x || !weight || !y || y == sum)) return GDN2_ERR_INVALID;
     const void *ptrs[] = {x, residual, weight, bias, y, sum};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;

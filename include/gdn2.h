@@ -385,7 +385,8 @@ int gdn2_chunk_bwd_kept(const void *q, const void *k, const void *v, const float
  * slot_out. Several sequences may start from one slot; no slot may be written
  * by two sequences of a call, nor written by one and read by another. Slots
  * that no sequence writes, and rows of o behind the last sequence, are left as
- * they were. Unlike elsewhere, log_alpha may be -infinity (a full forget).
+ * they were. o overlaps no input. Unlike elsewhere, log_alpha may be -infinity
+ * (a full forget).
  * A NaN or infinity in a token reaches that token and later ones of its
  * sequence, never an earlier token or a prefix kept without it.
  *
@@ -463,7 +464,7 @@ int gdn2_prologue_bwd(const void *q_raw, const void *k_raw, const void *v_raw, c
  *   y            [rows, cols] out_dtype
  *   sum          [rows, cols] in_dtype, or NULL: receives h, rounded
  * y and sum may each be x or residual itself (same type), but must not overlap
- * an input otherwise, nor each other. mean and variance are those of the
+ * an input otherwise, nor each other (y == sum: GDN2_ERR_INVALID). mean and variance are those of the
  * unrounded h, in fp32.
  *
  * gdn2_layer_norm_bwd: from dy = dL/dy (out_dtype of the forward) and h (the

@@ -279,3 +279,41 @@ def test_pool_past_32_bit_offsets():
     (o_ref, s_ref) = p.reference()
     ref.check('o', o[0].cpu().numpy(), o_ref)
     ref.check('state', state[at].cpu().numpy(), s_ref)
+
+
+@pytest.mark.parametrize('decay', [None, -12.0])
+@pytest.mark.parametrize('gates', ['channel', 'head'])
+def test_many_chains(gates, decay):
+    """More chains than half the compute units: a workgroup owns a whole chain. Ragged lengths,
+    scattered slots, commits; a decay that cuts blocks (e^-96 over eight tokens)."""
+    rng = np.random.default_rng(19)
+    N = 20
+    lens = rng.integers(0, 40, N).tolist()
+    slot = rng.permutation(N + 5)[:N].tolist()
+    commit = [int(rng.integers(0, n + 2)) for n in lens]
+    p = Batch(19, lens, H=8, HK=4, dk=128, dv=128, gates=gates, slots=N + 5, decay=decay)
+    check(p, f'many chains {gates} {decay}', slot_in=slot, commit=commit)
+
+
+def test_long_sequence():
+    check(Batch(20, [1000], H=1, dk=64, dv=64, dtype='f32'), 'long')
+
+
+def test_two_streams_share_a_pool():
+    """Two calls at once on two streams, on slots of one pool that do not meet."""
+    a, b = Batch(21, [9] * 8, H=4, dk=64, dv=64, slots=16), Batch(22, [9] * 8, H=4, dk=64, dv=64, slots=16)
+    b.state = a.state
+    (args_a, state, cu), (args_b, _, _) = a.gpu(), b.gpu()
+    sa, sb = ints(list(range(0, 16, 2))), ints(list(range(1, 16, 2)))
+    torch.cuda.synchronize()
+    outs = {}
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s, args, slot, name in ((streams[0], args_a, sa, 'a'), (streams[1], args_b, sb, 'b')):
+        with torch.cuda.stream(s):
+            outs[name] = gdn2.recurrent_fwd(*args, state, cu, slot_in=slot)
+    torch.cuda.synchronize()
+    for p, slot, name in ((a, sa, 'a'), (b, sb, 'b')):
+        at = slot.cpu().numpy()
+        (o_ref, s_ref) = p.reference(slot_in=at)
+        ref.check(f'o {name}', outs[name][0].cpu().numpy(), o_ref)
+        ref.check(f'state {name}', state.cpu().numpy()[at], (s_ref[0][at], s_ref[1][at]))

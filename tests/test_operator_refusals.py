@@ -98,7 +98,7 @@ def test_prologue_bwd_workspace():
 
 
 def layer_norm_fwd(**kw):
-    a = dict(x=P, res=P, w=P, b=P, y=P, s=P, rows=4, cols=100, eps=1e-5, dt=BF16, odt=F32)
+    a = dict(x=P, res=P, w=P, b=P, y=P, s=2 * P, rows=4, cols=100, eps=1e-5, dt=BF16, odt=F32)
     a.update(kw)
     return lib.gdn2_layer_norm_fwd(*(a[n] for n in a))
 
@@ -116,7 +116,7 @@ LN = [(dict(w=None), INVALID), (dict(rows=-1), INVALID), (dict(cols=0), INVALID)
 
 
 @pytest.mark.parametrize('kw,status', LN + [(dict(x=None), INVALID), (dict(y=None), INVALID), (dict(s=P + 2), INVALID),
-                                            (dict(res=P + 8), INVALID)])
+                                            (dict(res=P + 8), INVALID), (dict(s=P), INVALID)])
 def test_layer_norm_fwd_rejects(kw, status):
     assert layer_norm_fwd(**kw) == status
 
