@@ -13,10 +13,11 @@
 // a wave or a workgroup), E packs of eight elements each; mean and variance are
 // two passes over the registers, so an offset far from zero costs no
 // precision. Rows pass through once, so they are loaded and stored past the
-// caches (non-temporal: 65536 x 2048 bf16 with residual and sum 201 -> 193 us,
-// backward 159 -> 143 us). Everything is fp32; y, sum and dh are rounded once, as they are
-// stored. The statistics are those of the unrounded sum. Rows too long for
-// the registers are read again for each pass (they stay in the L2).
+// caches (65536 x 2048 bf16 with residual and sum 193 us instead of 201, and 182
+// with the weights loaded as vectors, 5.9 TB/s; backward 143 us instead of 159,
+// now 137, 5.9 TB/s). Everything is fp32; y, sum and dh are rounded once, as
+// they are stored. The statistics are those of the unrounded sum. Rows too long
+// for the registers are read again for each pass (they stay in the L2).
 //
 // The backward takes the sum h and forms its statistics anew: the row is in
 // registers anyway, and its gradient is then that of the h it was given.
@@ -35,25 +36,55 @@ template <int TPR> struct RowShape {
     static constexpr int RPB = NT / TPR;               // rows of a workgroup
 };
 
-// What a lane holds: pack e of thread p of a row, n(e) elements of it there
-// (AL: all eight or none).
-template <int TPR, bool AL> struct RowPart {
+// How a row of `cols` elements falls into packs of eight: in whole ones; or
+// the last pack reaches back over its neighbour's elements, so that no lane
+// loads element by element; or the row is shorter than a pack.
+enum class Packs { kWhole, kOdd, kFew };
+
+// What a lane holds: pack e of thread p of a row, elements at(e) .. at(e) + 7.
+// mine(e, i): element i counts here (a row's sums take each element once; what
+// a lane holds twice it computes and stores twice, with the same bits).
+template <int TPR, Packs P> struct RowPart {
     int p, cols;
     __device__ __forceinline__ int col(int e) const { return (p + e * TPR) * 8; }
-    __device__ __forceinline__ int n(int e) const { return cols - col(e); }
-    __device__ __forceinline__ bool has(int e, int i) const { return (AL ? col(e) : col(e) + i) < cols; }
+    __device__ __forceinline__ bool any(int e) const { return col(e) < cols; }
+    __device__ __forceinline__ int at(int e) const { return P == Packs::kOdd ? min(col(e), cols - 8) : col(e); }
+    __device__ __forceinline__ bool mine(int e, int i) const
+    {
+        if (P == Packs::kWhole) return any(e);
+        if (P == Packs::kOdd) return at(e) + i >= col(e);
+        return col(e) + i < cols;
+    }
     template <bool NT = true, typename T> __device__ __forceinline__ void load(Pack8<T> &x, const T *row, int e) const
     {
-        x.zero();
-        if (n(e) > 0) x.template load<AL, NT>(row + col(e), n(e));
+        if constexpr (P == Packs::kOdd) {
+            x.template load<false, NT>(row + at(e));
+        } else if constexpr (P == Packs::kWhole) {
+            x.zero();
+            if (any(e)) x.template load<true, NT>(row + col(e));
+        } else {
+            x.load_some(row + col(e), cols - col(e));
+        }
+    }
+    // its own elements, zeros for others (in whole and few packs those are zeros as loaded)
+    __device__ __forceinline__ float own(float v, int e, int i) const
+    {
+        return P == Packs::kOdd && !mine(e, i) ? 0.f : v;
     }
     template <typename T> __device__ __forceinline__ void store(T *row, const float (&x)[8], int e) const
     {
-        if (n(e) > 0) store8<AL>(row + col(e), x, n(e));
+        if (!any(e)) return;
+        if constexpr (P == Packs::kFew) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (mine(e, i)) store1(row + col(e) + i, x[i]);
+        } else {
+            store8<P == Packs::kWhole>(row + at(e), x);
+        }
     }
 };
 
-template <typename In, typename Out, bool AL, int TPR, int E, bool RES>
+template <typename In, typename Out, Packs P, int TPR, int E, bool RES>
 __global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_fwd_kernel(
     const In *x, const In *res, const float *__restrict__ weight, const float *__restrict__ bias, Out *y, In *sum,
     int64_t rows, int cols, float inv_n, float eps)
@@ -61,7 +92,7 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_fwd_kernel(
     constexpr int RPB = RowShape<TPR>::RPB;
     __shared__ float red[TPR > 64 ? TPR / 64 : 1];
     const int grp = threadIdx.x / TPR;
-    const RowPart<TPR, AL> part = {(int)threadIdx.x % TPR, cols};
+    const RowPart<TPR, P> part = {(int)threadIdx.x % TPR, cols};
     float wv[E][8], bv[E][8];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -91,7 +122,7 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_fwd_kernel(
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 h[e][i] = RES ? px[e].get(i) + pr[e].get(i) : px[e].get(i);
-                s[0] += h[e][i];
+                s[0] += part.own(h[e][i], e, i);
             }
         row_sums<TPR>(s, red);
         const float mean = s[0] * inv_n;
@@ -99,7 +130,7 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_fwd_kernel(
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[0] += part.has(e, i) ? (h[e][i] - mean) * (h[e][i] - mean) : 0.f;
+            for (int i = 0; i < 8; ++i) s[0] += part.mine(e, i) ? (h[e][i] - mean) * (h[e][i] - mean) : 0.f;
         row_sums<TPR>(s, red);
         const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
         if (live)
@@ -141,7 +172,7 @@ __global__ __launch_bounds__(1024) void ln_fwd_long_kernel(
 }
 
 // Gradient. part: [gridDim.x][2][cols], this workgroup's sums of dy xh and dy.
-template <typename In, typename Dy, bool AL, int TPR, int E, bool SUM>
+template <typename In, typename Dy, Packs P, int TPR, int E, bool SUM>
 __global__ __launch_bounds__((RowShape<TPR>::NT)) __attribute__((amdgpu_waves_per_eu(TPR > 256 ? 4 : 2))) void ln_bwd_kernel(
     const Dy *dy, const In *h, const float *__restrict__ weight, const In *dsum, In *dh, float *__restrict__ partial,
     int64_t rows, int cols, float inv_n, float eps)
@@ -149,7 +180,7 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) __attribute__((amdgpu_waves_pe
     constexpr int RPB = RowShape<TPR>::RPB;
     __shared__ float red[TPR > 64 ? 2 * (TPR / 64) : 1];
     const int grp = threadIdx.x / TPR;
-    const RowPart<TPR, AL> part = {(int)threadIdx.x % TPR, cols};
+    const RowPart<TPR, P> part = {(int)threadIdx.x % TPR, cols};
     float wv[E][8], dw[E][8], db[E][8];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -177,8 +208,8 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) __attribute__((amdgpu_waves_pe
         for (int e = 0; e < E; ++e)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                s[0] += ph[e].get(i);
-                s[1] += pd[e].get(i) * wv[e][i];
+                s[0] += part.own(ph[e].get(i), e, i);
+                s[1] += part.own(pd[e].get(i) * wv[e][i], e, i);
             }
         row_sums<TPR>(s, red);
         const float mean = s[0] * inv_n, gm = s[1] * inv_n;
@@ -187,7 +218,7 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) __attribute__((amdgpu_waves_pe
         for (int e = 0; e < E; ++e)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float c = part.has(e, i) ? ph[e].get(i) - mean : 0.f;
+                const float c = part.mine(e, i) ? ph[e].get(i) - mean : 0.f;
                 s[0] += c * c;
                 s[1] += c * (pd[e].get(i) * wv[e][i]);
             }
@@ -222,7 +253,9 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) __attribute__((amdgpu_waves_pe
 #pragma unroll
         for (int e = 0; e < 2 * E; ++e) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[grp][part.p * 8 + i] = e < E ? dw[e % E][i] : db[e % E][i];
+            for (int i = 0; i < 8; ++i)
+                if (P != Packs::kOdd || part.mine(e % E, i))
+                    acc[grp][part.at(e % E) - e % E * TPR * 8 + i] = e < E ? dw[e % E][i] : db[e % E][i];
             __syncthreads();
             for (int c = threadIdx.x; c < TPR * 8; c += RowShape<TPR>::NT) {
                 const int cc = (e % E) * TPR * 8 + c;
@@ -279,17 +312,22 @@ __global__ __launch_bounds__(1024) void ln_bwd_long_kernel(
 
 // ---- launch ------------------------------------------------------------------
 
-// Calls f with the (AL, TPR, E) that hold a row of `cols` elements in
-// registers, or returns false (the long-row kernels take it). AL: rows keep
-// 16-byte alignment. A wave a row as long as its registers hold one (2048
-// elements; 65536 x 2048 bf16 backward: 142 us, 222 with a workgroup a row).
+// Calls f with the (packs, TPR, E) that hold a row of `cols` elements in
+// registers, or returns false (the long-row kernels take it). A wave a row as
+// long as its registers hold one (2048 elements; 65536 x 2048 bf16 backward:
+// 137 us, 222 with a workgroup a row).
+template <Packs P> using PacksOf = std::integral_constant<Packs, P>;
 template <typename F> static bool for_row_shape(int cols, F f)
 {
     auto go = [&](auto t, auto e) {
-        if (cols % 8 == 0) f(std::true_type{}, t, e);
-        else f(std::false_type{}, t, e);
+        if (cols % 8 == 0) f(PacksOf<Packs::kWhole>{}, t, e);
+        else f(PacksOf<Packs::kOdd>{}, t, e);
         return true;
     };
+    if (cols < 8) {
+        f(PacksOf<Packs::kFew>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+        return true;
+    }
 #define GDN2_ROW(T, E) \
     if (cols <= 8 * T * E) return go(std::integral_constant<int, T>{}, std::integral_constant<int, E>{});
     GDN2_ROW(8, 1)
@@ -314,12 +352,12 @@ template <typename In, typename Out> static void ln_fwd(const LayerNormArgs &a, 
         hipLaunchKernelGGL(kern, dim3(grid), dim3(nt), 0, st, (const In *)a.x, (const In *)a.residual, a.weight, a.bias,
                            (Out *)a.y, (In *)a.sum, a.rows, a.cols, inv_n, a.eps);
     };
-    const bool held = for_row_shape(a.cols, [&](auto al, auto t, auto e) {
-        constexpr bool AL = decltype(al)::value;
+    const bool held = for_row_shape(a.cols, [&](auto packs, auto t, auto e) {
+        constexpr Packs P = decltype(packs)::value;
         constexpr int T = decltype(t)::value, E = decltype(e)::value;
         const int grid = ln_grid(a.rows, RowShape<T>::RPB, kLnFwdGrid);
-        if (a.residual) args(ln_fwd_kernel<In, Out, AL, T, E, true>, grid, RowShape<T>::NT);
-        else args(ln_fwd_kernel<In, Out, AL, T, E, false>, grid, RowShape<T>::NT);
+        if (a.residual) args(ln_fwd_kernel<In, Out, P, T, E, true>, grid, RowShape<T>::NT);
+        else args(ln_fwd_kernel<In, Out, P, T, E, false>, grid, RowShape<T>::NT);
     });
     if (!held) args(ln_fwd_long_kernel<In, Out>, ln_grid(a.rows, 1, kLnFwdGrid), 1024);
 }
@@ -332,11 +370,11 @@ template <typename In, typename Dy> static void ln_bwd(const LayerNormBwdArgs &a
                            (const In *)a.dsum, (In *)a.dh, (float *)a.workspace, a.rows, a.cols, inv_n, a.eps);
     };
     const int grid = ln_bwd_parts(a.rows, a.cols);
-    const bool held = for_row_shape(a.cols, [&](auto al, auto t, auto e) {
-        constexpr bool AL = decltype(al)::value;
+    const bool held = for_row_shape(a.cols, [&](auto packs, auto t, auto e) {
+        constexpr Packs P = decltype(packs)::value;
         constexpr int T = decltype(t)::value, E = decltype(e)::value;
-        if (a.dsum) args(ln_bwd_kernel<In, Dy, AL, T, E, true>, grid, RowShape<T>::NT);
-        else args(ln_bwd_kernel<In, Dy, AL, T, E, false>, grid, RowShape<T>::NT);
+        if (a.dsum) args(ln_bwd_kernel<In, Dy, P, T, E, true>, grid, RowShape<T>::NT);
+        else args(ln_bwd_kernel<In, Dy, P, T, E, false>, grid, RowShape<T>::NT);
     });
     if (!held) args(ln_bwd_long_kernel<In, Dy>, grid, 1024);
 }

@@ -83,7 +83,7 @@ template <> struct Raw4<float> {
 };
 
 template <typename In, int DK, int DV, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW < 4 ? 3 : 4))) void recurrent_kernel(RecParams a)
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1 ? 1 : NW < 4 ? 3 : 4))) void recurrent_kernel(RecParams a)
 {
     constexpr int C = kRecTokens, NT = 64 * NW, NR = DK / 16, WGC = DV / (16 * NW);   // WGC: workgroups of a chain
     constexpr int XS = DK + 4;    // row stride of the fragment tiles (16-byte rows)

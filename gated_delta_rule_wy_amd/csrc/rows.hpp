@@ -11,33 +11,28 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 // Eight consecutive elements as they lie in memory, kept packed until use (the
 // loads of a row are issued together), NT: past the caches. AL: the address is a
-// multiple of 16 bytes, and all eight are there. Otherwise it is any address
-// of an element (the memory pipe takes a 16-byte load at any), and only the
-// first n are (the others are zeros).
+// multiple of 16 bytes; otherwise it is that of any element (the memory pipe
+// takes a 16-byte load at any).
 typedef u4 u4_any __attribute__((aligned(2)));
 typedef f4 f4_any __attribute__((aligned(4)));
-
-template <bool NT, typename T> __device__ __forceinline__ T get_as(const T *p)
-{
-    if constexpr (NT) return __builtin_nontemporal_load(p);
-    else return *p;
-}
 
 template <typename In> struct Pack8;
 template <> struct Pack8<uint16_t> {
     u4 r;
-    template <bool AL, bool NT> __device__ __forceinline__ void load(const uint16_t *p, int n)
+    template <bool AL, bool NT> __device__ __forceinline__ void load(const uint16_t *p)
     {
-        if constexpr (AL) {
-            r = get_as<NT>(reinterpret_cast<const u4 *>(p));
-        } else if (n >= 8) {
-            r = get_as<NT>(reinterpret_cast<const u4_any *>(p));
-        } else {
-            zero();
+        if constexpr (AL && NT) r = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p));
+        else if constexpr (AL) r = *reinterpret_cast<const u4 *>(p);
+        else if constexpr (NT) r = __builtin_nontemporal_load(reinterpret_cast<const u4_any *>(p));
+        else r = *reinterpret_cast<const u4_any *>(p);
+    }
+    // the first n elements, zeros behind them
+    __device__ __forceinline__ void load_some(const uint16_t *p, int n)
+    {
+        zero();
 #pragma unroll
-            for (int i = 0; i < 7; ++i)
-                if (i < n) r[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-        }
+        for (int i = 0; i < 8; ++i)
+            if (i < n) r[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
     }
     __device__ __forceinline__ float get(int i) const
     {
@@ -47,20 +42,22 @@ template <> struct Pack8<uint16_t> {
 };
 template <> struct Pack8<float> {
     f4 r[2];
-    template <bool AL, bool NT> __device__ __forceinline__ void load(const float *p, int n)
+    template <bool AL, bool NT> __device__ __forceinline__ void load(const float *p)
     {
-        if constexpr (AL) {
-            r[0] = get_as<NT>(reinterpret_cast<const f4 *>(p));
-            r[1] = get_as<NT>(reinterpret_cast<const f4 *>(p) + 1);
-        } else if (n >= 8) {
-            r[0] = get_as<NT>(reinterpret_cast<const f4_any *>(p));
-            r[1] = get_as<NT>(reinterpret_cast<const f4_any *>(p) + 1);
-        } else {
-            zero();
 #pragma unroll
-            for (int i = 0; i < 7; ++i)
-                if (i < n) r[i >> 2][i & 3] = p[i];
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (AL && NT) r[i] = __builtin_nontemporal_load(reinterpret_cast<const f4 *>(p) + i);
+            else if constexpr (AL) r[i] = reinterpret_cast<const f4 *>(p)[i];
+            else if constexpr (NT) r[i] = __builtin_nontemporal_load(reinterpret_cast<const f4_any *>(p) + i);
+            else r[i] = reinterpret_cast<const f4_any *>(p)[i];
         }
+    }
+    __device__ __forceinline__ void load_some(const float *p, int n)
+    {
+        zero();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) r[i >> 2][i & 3] = p[i];
     }
     __device__ __forceinline__ float get(int i) const { return r[i >> 2][i & 3]; }
     __device__ __forceinline__ void zero() { r[0] = r[1] = f4zero(); }
@@ -79,35 +76,24 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b)
 
 __device__ __forceinline__ uint16_t bf16_of(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 
-// Eight floats to memory in the output type, past the caches; AL and n as in
+// Eight floats to memory in the output type, past the caches; AL as in
 // Pack8::load.
-template <bool AL> __device__ __forceinline__ void store8(float *p, const float (&x)[8], int n)
+template <bool AL> __device__ __forceinline__ void store8(float *p, const float (&x)[8])
 {
     const f4 a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
     if constexpr (AL) {
         __builtin_nontemporal_store(a, reinterpret_cast<f4 *>(p));
         __builtin_nontemporal_store(b, reinterpret_cast<f4 *>(p) + 1);
-    } else if (n >= 8) {
+    } else {
         __builtin_nontemporal_store(a, reinterpret_cast<f4_any *>(p));
         __builtin_nontemporal_store(b, reinterpret_cast<f4_any *>(p) + 1);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < n) p[i] = x[i];
     }
 }
-template <bool AL> __device__ __forceinline__ void store8(uint16_t *p, const float (&x)[8], int n)
+template <bool AL> __device__ __forceinline__ void store8(uint16_t *p, const float (&x)[8])
 {
     const u4 r = {bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7])};
-    if constexpr (AL) {
-        __builtin_nontemporal_store(r, reinterpret_cast<u4 *>(p));
-    } else if (n >= 8) {
-        __builtin_nontemporal_store(r, reinterpret_cast<u4_any *>(p));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < n) p[i] = bf16_of(x[i]);
-    }
+    if constexpr (AL) __builtin_nontemporal_store(r, reinterpret_cast<u4 *>(p));
+    else __builtin_nontemporal_store(r, reinterpret_cast<u4_any *>(p));
 }
 // one float
 __device__ __forceinline__ void store1(float *p, float x) { *p = x; }

@@ -152,6 +152,28 @@ def test_in_place(cols):
     assert all(torch.equal(g[n], g2[n]) for n in g)
 
 
+@pytest.mark.parametrize('dtype', ['bf16', 'f32'])
+@pytest.mark.parametrize('cols', [1, 3, 9, 15, 65, 127, 129, 257, 521, 1025, 2049, 4097, 8191, 16383, 16385])
+def test_in_place_odd_widths(cols, dtype):
+    """Rows that do not fall into whole packs: what lanes hold twice is written as it is read, the rows around
+    stay whole, and a row of NaN stays one row."""
+    print(f'[in place] cols={cols} {dtype}', flush=True)
+    x, r, dy, w, b = make(cols + 3, 37, cols, dtype)
+    x[17] = np.nan
+    gx, gr = gpu(x, dtype), gpu(r, dtype)
+    y, h = gdn2.layer_norm_fwd(gx, gpu(w), gpu(b), gr, output_sum=True)
+    bad = torch.isnan(y).any(1)
+    assert bad[17] and int(bad.sum()) == 1 and bool(torch.isnan(y[17]).all())
+    x2, r2 = gx.clone(), gr.clone()
+    gdn2.layer_norm_fwd(x2, gpu(w), gpu(b), r2, out=x2, sum_out=r2)
+    assert torch.equal(y.nan_to_num(7.), x2.nan_to_num(7.)) and torch.equal(h.nan_to_num(7.), r2.nan_to_num(7.))
+    d, hr = gpu(dy, dtype), gr
+    g = gdn2.layer_norm_bwd(d, hr, gpu(w))
+    d2 = d.clone()
+    g2 = gdn2.layer_norm_bwd(d2, hr, gpu(w), out=d2)
+    assert all(torch.equal(g[n], g2[n]) for n in g)
+
+
 def test_leading_axes_and_determinism():
     x, r, dy, w, b = make(6, 4 * 5 * 60, 136, 'bf16')
     sh = (4, 5, 60, 136)
