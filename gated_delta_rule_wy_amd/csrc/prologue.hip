@@ -586,6 +586,18 @@ static ProParams pro_params(const PrologueArgs &a, int V, int64_t tiles, int til
     return p;
 }
 
+// Tokens a thread of V channels walks over: as many as leave 12 waves a compute
+// unit, between 8 and `most` (a tile reads three rows before its own, backward
+// also three after it). Backward, 4 x 2048 tokens, 16 heads of 128, fp32: 199 us
+// so, 248 with 8 waves, 210 with 16; 300 bf16 tokens: 16.6 us, 18.9 with no
+// tile below 16 tokens. Forward, 300 bf16 tokens: 9.3 us, 22 with tiles of 64.
+static int tile_of(long long tokens, long long channels, int V, long long most)
+{
+    const long long t = tokens * (channels / V) / (256LL * 12 * 64);
+    return (int)std::max(8LL, std::min(most, (t + 3) / 4 * 4));
+}
+int prologue_bwd_tile(long long tokens, long long channels) { return tile_of(tokens, channels, kBwdV, 256); }
+
 // Sequences of at most this many tokens are walked by one thread a channel
 // group each, which then also writes their histories (one launch).
 constexpr int kOwnTokens = 16;
@@ -594,7 +606,9 @@ template <typename In> static hipError_t prologue_fwd_t(const PrologueArgs &a, h
 {
     const bool own = a.T <= kOwnTokens, hist = a.hist_out[0] != nullptr;
     const int64_t tokens = tokens_of(a);
-    const int tile = 64;
+    int64_t channels = 0;
+    for (int z = 0; z < 3; ++z) channels += a.heads[z] * a.d[z];
+    const int tile = tile_of(tokens, channels, kFwdV, 64);
     int blocks = 0;
     const ProParams p = pro_params(a, kFwdV, own ? a.N : (tokens + tile - 1) / tile, tile, &blocks);
     if (blocks > 0 && (tokens > 0 || (own && hist))) {
@@ -617,16 +631,6 @@ template <typename In> static hipError_t prologue_fwd_t(const PrologueArgs &a, h
 hipError_t launch_prologue_fwd(const PrologueArgs &a, hipStream_t st)
 {
     return a.bf16 ? prologue_fwd_t<uint16_t>(a, st) : prologue_fwd_t<float>(a, st);
-}
-
-// Tokens a backward thread walks over: as many as leave 12 waves a compute
-// unit, between 8 and 256 (a tile reads three rows before and three after its
-// own). 4 x 2048 tokens, 16 heads of 128, fp32: 199 us so, 248 with 8 waves,
-// 210 with 16; 300 bf16 tokens: 16.6 us, 18.9 with no tile below 16 tokens.
-int prologue_bwd_tile(long long tokens, long long channels)
-{
-    const long long t = tokens * (channels / kBwdV) / (256LL * 12 * 64);
-    return (int)std::max(8LL, std::min(256LL, (t + 3) / 4 * 4));
 }
 
 size_t prologue_bwd_workspace(long long tokens, long long channels)

@@ -90,7 +90,7 @@ def check_bwd(p, label, slot_in=None):
 
 
 SHORT = [1, 0, 2, 3, 0, 4, 5]                       # 15 tokens: one thread walks a sequence
-LONG = [1, 0, 33, 2, 64, 0, 0, 3, 31, 5, 100, 32]   # tiles of 32 that sequences start and end in
+LONG = [1, 0, 33, 2, 64, 0, 0, 3, 31, 5, 100, 32]   # tiles that sequences start and end in
 
 
 @pytest.mark.parametrize('dtype', ['bf16', 'f32'])
