@@ -10,6 +10,11 @@ Recurrence (snilld.dk, "Hvad Gated DeltaNet-2 ændrer", update equation), per
 sequence and head, state S in R^{dk x dv}:
     S_t = (I - k_t (b_t * k_t)^T) Diag(exp(log_alpha_t)) S_{t-1} + k_t (w_t * v_t)^T
     o_t = S_t^T q_t
+
+Around it, for a whole layer: ``prologue_fwd`` / ``prologue_bwd`` (short
+convolution, unit norm, sigmoid), ``recurrent_fwd`` (the recurrence over a few
+tokens a sequence, its states in a pool) and ``layer_norm_fwd`` /
+``layer_norm_bwd``.
 """
 from __future__ import annotations
 
