@@ -14,9 +14,10 @@
 // neighbours, and its norm a sum over them) and walks along the tokens with the
 // last three inputs in registers, eight rows of loads ahead. Few channels a
 // thread, so that many waves fit: forward over 32 packed sequences of up to
-// 2048 tokens, 16 heads of 128, bf16: 274 us with four (5.4 TB/s), 296 with
-// eight; backward over 8 of up to 4096: 367 us with two (5.5 TB/s), 379 with
-// four. All sums are fp32; outputs are rounded once.
+// 2048 tokens, 16 heads of 128, bf16: 274 us with four, 296 with eight, and 267
+// (5.6 TB/s) since the histories no longer take a launch of their own; backward
+// over 8 of up to 4096: 368 us with two (5.4 TB/s), 379 with four. All sums are
+// fp32; outputs are rounded once.
 #include "gdn2_launch.hpp"
 #include "rows.hpp"
 
@@ -65,15 +66,22 @@ struct SeqTable {
             if (end(++i) > t) break;
         return i;
     }
-    // the last sequence that starts at or before token t
+    // the last sequence that starts at or before token t (eighths of what is
+    // left at a time: the loads of a step are under way together)
     __device__ __forceinline__ int of(int t) const
     {
         if (!cu) return min(t / T, N - 1);
         int lo = 0, hi = N - 1;
         while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cu[mid] <= t) lo = mid;
-            else hi = mid - 1;
+            const int step = (hi - lo) / 8 + 1;
+            int at = lo;
+#pragma unroll
+            for (int j = 1; j < 8; ++j) {
+                const int m = min(lo + j * step, hi);
+                if (cu[m] <= t) at = max(at, m);
+            }
+            lo = at;
+            hi = min(hi, at + step - 1);
         }
         return lo;
     }
@@ -139,6 +147,7 @@ struct ProParams {
     SeqTable sq;
     const int32_t *slot_in, *slot_out, *commit;
     int slots, tile;     // tokens a thread walks over
+    int empty0;          // first of the workgroups for sequences without tokens
 };
 
 // This thread's tile and first channel, V of them: false where it has none
@@ -206,8 +215,52 @@ __device__ void gate_fwd(const ProGate &gt, int64_t total, int block)
     }
 }
 
+template <typename In, int V>
+__device__ __forceinline__ void store_history(const PackV<In, V> (&r)[3], const ProTensor &t, int slot, int ch)
+{
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+        r[j].store((In *)t.hout + ((((size_t)slot * t.heads + (ch >> t.ld)) * 3 + j) << t.ld) + (ch & (t.d - 1)));
+}
+
+// The history that sequence i (tokens s0 .. s0 + len - 1) leaves: the three raw
+// inputs up to its last kept token, read before any is written.
+template <typename In, int V>
+__device__ __forceinline__ void put_history(const ProTensor &t, const ProParams &p, int i, int s0, int len, int ch)
+{
+    const int slot = p.slot_out ? p.slot_out[i] : (p.slot_in ? p.slot_in[i] : i);
+    if ((unsigned)slot >= (unsigned)p.slots) return;
+    const int keep = p.commit ? min(max(p.commit[i], 0), len) : len;
+    PackV<In, V> r[3];
+    load_window<In, V>(r, t, p, i, s0, keep - 3, ch);
+    store_history<In, V>(r, t, slot, ch);
+}
+
+// A sequence without tokens: its history goes from slot to slot. One workgroup
+// a sequence, 8 elements a thread.
+template <typename In> __device__ void empty_history(const ProParams &p, int i)
+{
+    if (p.sq.end(i) != p.sq.start(i)) return;
+    const int in = p.slot_in ? p.slot_in[i] : i, out = p.slot_out ? p.slot_out[i] : in;
+    if ((unsigned)out >= (unsigned)p.slots) return;
+    for (int z = 0; z < 3; ++z) {
+        const ProTensor &t = p.t[z];
+        const size_t n = (size_t)t.heads * t.d * 3;
+        if (t.hin == t.hout && in == out) continue;
+        for (size_t c = threadIdx.x * 8; c < n; c += kNT * 8) {
+            PackV<In, 8> r;
+            r.zero();
+            if (t.hin && (unsigned)in < (unsigned)p.slots) r.load((const In *)t.hin + in * n + c);
+            r.store((In *)t.hout + out * n + c);
+        }
+    }
+}
+
 // OWN: the thread's tile is one whole sequence (short ones), and it also
-// writes the sequence's new history, after reading the old one.
+// writes the sequence's new history, after reading the old one. Otherwise
+// tiles cut sequences, and the thread in whose tile a sequence begins takes its
+// first three tokens whole, so that it alone reads the history, and writes the
+// new one (which may take the old one's place).
 template <typename In, bool OWN>
 __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
 {
@@ -220,6 +273,10 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
             gate_fwd<In>(p.g[z], total, bid - p.g[z].block0);
             return;
         }
+    if (!OWN && bid >= p.empty0) {
+        empty_history<In>(p, bid - p.empty0);
+        return;
+    }
     const int z = bid >= p.t[2].block0 ? 2 : (bid >= p.t[1].block0 ? 1 : 0);
     const ProTensor &t = p.t[z];
     const size_t W = (size_t)t.heads * t.d;
@@ -227,17 +284,25 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
     int64_t tl;
     int ch;
     if (!my_part<V>(t, bid - t.block0, tl, ch)) return;
-    int i, tb, te;
+    int i, tb, te, s0, s1, first = 0, bound = 0;   // sequences from `first` that begin before `bound` begin here
     if (OWN) {
         if (tl >= p.sq.N) return;   // (a head's lanes leave together)
         i = (int)tl;
-        tb = p.sq.start(i);
-        te = p.sq.end(i);
+        s0 = tb = p.sq.start(i);
+        s1 = te = p.sq.end(i);
     } else {
         if (tl * p.tile >= total) return;
         tb = (int)(tl * p.tile);
         te = min(tb + p.tile, total);
         i = p.sq.of(tb);
+        s0 = p.sq.start(i);
+        s1 = p.sq.end(i);
+        first = s0 < tb ? i + 1 : i;
+        bound = te;
+        if (s0 < tb) tb = max(tb, min(s0 + 3, s1));
+        if (tb >= te) return;
+        const int il = te <= s1 ? i : p.sq.next(i, te - 1), sl = p.sq.start(il);
+        if (sl >= tb) te = max(te, min(sl + 3, p.sq.end(il)));
     }
     const In *x = (const In *)t.x;
     In *y = (In *)t.y;
@@ -256,8 +321,17 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
 #pragma unroll
             for (int c = 0; c < V; ++c) old[j][c] = win[j].get(c);
     };
-    int s0 = p.sq.start(i), s1 = p.sq.end(i);
-    load_window<In, V>(win, t, p, i, s0, tb - s0 - 3, ch);
+    if (OWN) {
+        load_window<In, V>(win, t, p, i, s0, -3, ch);
+    } else if (s0 < tb && tb < s1) {   // in the midst of a sequence: behind its first three tokens
+#pragma unroll
+        for (int j = 0; j < 3; ++j) win[j].load(x + (size_t)(tb - 3 + j) * W + ch);
+    } else {                           // a sequence begins, this or a later one: the loop opens it
+#pragma unroll
+        for (int j = 0; j < 3; ++j) win[j].zero();
+        if (s0 == tb) --i;
+        s1 = tb;
+    }
     numbers();
     PackV<In, V> nxt[U];
     if (tb < te)
@@ -314,32 +388,13 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
         const int keep = p.commit ? min(max(p.commit[i], 0), te - tb) : te - tb;
         // (win holds the last three inputs, or the old history's)
         if (keep < te - tb) load_window<In, V>(win, t, p, i, tb, keep - 3, ch);
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-            win[j].store((In *)t.hout + ((((size_t)slot * t.heads + (ch >> t.ld)) * 3 + j) << t.ld) + (ch & (t.d - 1)));
+        store_history<In, V>(win, t, slot, ch);
+    } else if (t.hout) {
+        for (int j = first; j < p.sq.N && p.sq.start(j) < bound; ++j) {
+            const int b = p.sq.start(j), len = p.sq.end(j) - b;
+            if (len > 0) put_history<In, V>(t, p, j, b, len, ch);
+        }
     }
-}
-
-// New histories of sequences that several threads walked over. A thread owns
-// V channels of one sequence's three rows and reads them all before it writes.
-template <typename In> __global__ __launch_bounds__(kNT) void prologue_history_kernel(ProParams p)
-{
-    constexpr int V = 8;
-    const int bid = blockIdx.x;
-    const ProTensor &t = p.t[bid >= p.t[2].block0 ? 2 : (bid >= p.t[1].block0 ? 1 : 0)];
-    int64_t tl;
-    int ch;
-    if (!my_part<V>(t, bid - t.block0, tl, ch) || tl >= p.sq.N) return;
-    const int i = (int)tl;
-    const int slot = p.slot_out ? p.slot_out[i] : (p.slot_in ? p.slot_in[i] : i);
-    if ((unsigned)slot >= (unsigned)p.slots) return;
-    const int tb = p.sq.start(i), len = p.sq.end(i) - tb;
-    const int keep = p.commit ? min(max(p.commit[i], 0), len) : len;
-    PackV<In, V> h[3];
-    load_window<In, V>(h, t, p, i, tb, keep - 3, ch);
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-        h[j].store((In *)t.hout + ((((size_t)slot * t.heads + (ch >> t.ld)) * 3 + j) << t.ld) + (ch & (t.d - 1)));
 }
 
 // ---- backward ------------------------------------------------------------------
@@ -587,16 +642,17 @@ static ProParams pro_params(const PrologueArgs &a, int V, int64_t tiles, int til
 }
 
 // Tokens a thread of V channels walks over: as many as leave 12 waves a compute
-// unit, between 8 and `most` (a tile reads three rows before its own, backward
-// also three after it). Backward, 4 x 2048 tokens, 16 heads of 128, fp32: 199 us
-// so, 248 with 8 waves, 210 with 16; 300 bf16 tokens: 16.6 us, 18.9 with no
-// tile below 16 tokens. Forward, 300 bf16 tokens: 9.3 us, 22 with tiles of 64.
-static int tile_of(long long tokens, long long channels, int V, long long most)
+// unit, between `least` and `most` (a tile reads three rows before its own,
+// backward also three after it). Backward, 4 x 2048 tokens, 16 heads of 128,
+// fp32: 199 us so, 248 with 8 waves, 210 with 16; 300 bf16 tokens: 16.6 us with
+// 8 tokens a tile, 18.9 with 16. Forward, 300 bf16 tokens of one sequence: 10 us,
+// 22 with tiles of 64.
+static int tile_of(long long tokens, long long channels, int V, long long least, long long most)
 {
     const long long t = tokens * (channels / V) / (256LL * 12 * 64);
-    return (int)std::max(8LL, std::min(most, (t + 3) / 4 * 4));
+    return (int)std::max(std::max(1LL, least), std::min(most, t));
 }
-int prologue_bwd_tile(long long tokens, long long channels) { return tile_of(tokens, channels, kBwdV, 256); }
+int prologue_bwd_tile(long long tokens, long long channels) { return tile_of(tokens, channels, kBwdV, 8, 256); }
 
 // Sequences of at most this many tokens are walked by one thread a channel
 // group each, which then also writes their histories (one launch).
@@ -608,22 +664,19 @@ template <typename In> static hipError_t prologue_fwd_t(const PrologueArgs &a, h
     const int64_t tokens = tokens_of(a);
     int64_t channels = 0;
     for (int z = 0; z < 3; ++z) channels += a.heads[z] * a.d[z];
-    const int tile = tile_of(tokens, channels, kFwdV, 64);
+    // (a tile's sequences come one after the other, so no more than two of them on
+    // average: 256 packed sequences of one token 16 us, 21 with tiles of 8 tokens,
+    // and 19 with a tile each)
+    const int tile = tile_of(tokens, channels, kFwdV, std::min<long long>(4, tokens / a.N),
+                             std::min<long long>(64, 2 * tokens / a.N));
     int blocks = 0;
-    const ProParams p = pro_params(a, kFwdV, own ? a.N : (tokens + tile - 1) / tile, tile, &blocks);
-    if (blocks > 0 && (tokens > 0 || (own && hist))) {
-        prof_before("gdn2_prologue_fwd", st);
-        if (own) hipLaunchKernelGGL((prologue_fwd_kernel<In, true>), dim3(blocks), dim3(kNT), 0, st, p);
-        else hipLaunchKernelGGL((prologue_fwd_kernel<In, false>), dim3(blocks), dim3(kNT), 0, st, p);
-        prof_after(st);
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
-    }
-    if (own || !hist) return hipSuccess;
-    int hblocks = 0;
-    ProParams h = pro_params(a, 8, a.N, 0, &hblocks);
-    prof_before("gdn2_prologue_history", st);
-    hipLaunchKernelGGL((prologue_history_kernel<In>), dim3(h.g[0].block0), dim3(kNT), 0, st, h);
+    ProParams p = pro_params(a, kFwdV, own ? a.N : (tokens + tile - 1) / tile, tile, &blocks);
+    p.empty0 = blocks;
+    if (!own && hist && a.cu_seqlens) blocks += a.N;
+    if (blocks == 0 || (tokens == 0 && !hist)) return hipSuccess;
+    prof_before("gdn2_prologue_fwd", st);
+    if (own) hipLaunchKernelGGL((prologue_fwd_kernel<In, true>), dim3(blocks), dim3(kNT), 0, st, p);
+    else hipLaunchKernelGGL((prologue_fwd_kernel<In, false>), dim3(blocks), dim3(kNT), 0, st, p);
     prof_after(st);
     return hipGetLastError();
 }

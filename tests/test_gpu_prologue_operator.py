@@ -124,6 +124,30 @@ def test_histories(lens, inplace, dtype):
     check_bwd(p, 'bwd slots', slot)
 
 
+@pytest.mark.parametrize('dtype', ['bf16', 'f32'])
+@pytest.mark.parametrize('top', [1, 2, 3, 4, 6, 9])
+def test_packed_short_sequences(top, dtype):
+    """Sequences of 0 .. top tokens, packed: tiles of one to four tokens that several sequences share and that cut
+    sequences within their first three tokens; the pools in place, kept in their slots or moved."""
+    rng = np.random.default_rng(top)
+    lens = rng.integers(0, top + 1, 61).tolist()
+    N = len(lens)
+    commit = rng.integers(-1, top + 2, N).tolist()
+    perm = rng.permutation(2 * N + 3)
+    p = Batch(20 + top, lens, H=4, HK=2, dk=32, dv=64, dtype=dtype, slots=2 * N + 3)
+    check_fwd(p, f'kept {top}', True, slot_in=perm[:N].tolist())
+    check_fwd(p, f'commit {top}', True, slot_in=perm[:N].tolist(), commit=commit)
+    check_fwd(p, f'moved {top}', True, slot_in=perm[:N].tolist(), slot_out=perm[N:2 * N].tolist(), commit=commit)
+    check_bwd(p, f'bwd {top}', perm[:N].tolist())
+
+
+@pytest.mark.parametrize('N', [17, 70, 300])
+def test_packed_single_tokens(N):
+    p = Batch(40 + N, [1] * N, H=4, HK=4, dk=128, dv=128, slots=N + 2)
+    slot = np.random.default_rng(N).permutation(N + 2)[:N].tolist()
+    check_fwd(p, f'single {N}', True, slot_in=slot)
+
+
 @pytest.mark.parametrize('lens', [SHORT, LONG])
 def test_history_slots_none_forked_and_moved(lens):
     """None in, none out, two sequences from one slot, another slot out, negative and large commits."""
