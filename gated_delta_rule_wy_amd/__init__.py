@@ -565,6 +565,9 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+_data_ptr = torch.Tensor.data_ptr
+
+
 # The current stream's handle: current_stream() builds a Stream object around
 # it, most of the host's time of a small call (1.9 of 12 us).
 _raw_stream = getattr(torch._C, '_cuda_getCurrentRawStream', None) or (
@@ -605,7 +608,8 @@ def _heads(q, k, v, cu_seqlens, names):
     B, T, HK, dk = q.shape
     H, dv = v.shape[2:]
     _need(k, names[1], q.shape, dt, dev)
-    _need(q, names[0], q.shape, dt, dev)
+    if not q.is_contiguous():
+        raise ValueError(f'{names[0]}: must be contiguous')
     _need(v, names[2], (B, T, H, dv), dt, dev)
     if HK < 1 or H % HK:
         raise ValueError(f'{names[2]}: its {H} heads are not a multiple of the {HK} of {names[0]}')
@@ -717,14 +721,14 @@ def prologue_fwd(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor, 
         raise ValueError(f'conv_state: {slots} slots for {N} sequences (pass slot_in)')
     raw = (q_raw, k_raw, v_raw, b_logit, w_logit)
     if out is None:
-        out = tuple(torch.empty_like(x) for x in raw)
+        out = tuple(map(torch.empty_like, raw))
     else:
         if len(out) != 5:
             raise ValueError('out must be (q, k, v, b, w)')
         for n, t, x in zip('qkvbw', out, raw):
             _need(t, f'out[{n}]', x.shape, dt, dev)
-    _call(_lib.gdn2_prologue_fwd, 'gdn2_prologue_fwd', dev, *(x.data_ptr() for x in raw), gates, ctypes.byref(sc),
-          _addr(slot_in), _addr(slot_out), _addr(commit), *(x.data_ptr() for x in out), _addr(cu_seqlens), B, T, N, H,
+    _call(_lib.gdn2_prologue_fwd, 'gdn2_prologue_fwd', dev, *map(_data_ptr, raw), gates, ctypes.byref(sc),
+          _addr(slot_in), _addr(slot_out), _addr(commit), *map(_data_ptr, out), _addr(cu_seqlens), B, T, N, H,
           HK, slots, dk, dv, _CODES[dt])
     return tuple(out)
 
@@ -754,13 +758,14 @@ def prologue_bwd(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor, 
     like = raw if grad_dtype is dt else grads if grad_dtype is torch.float32 else None
     if like is None:
         like = [torch.empty(x.shape, dtype=grad_dtype, device=dev) for x in raw]
-    g = {n: torch.empty_like(x) for n, x in zip(('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit'), like)}
-    for n, x in zip('qkv', conv_weight):
-        g['weight_' + n] = torch.empty_like(x)
+    outs = tuple(map(torch.empty_like, like))
+    g = dict(zip(('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit'), outs))
+    taps = tuple(map(torch.empty_like, conv_weight))
+    g.update(zip(('weight_q', 'weight_k', 'weight_v'), taps))
     if conv_bias is not None:
-        for n, x in zip('qkv', conv_bias):
+        for n, x in zip(('bias_q', 'bias_k', 'bias_v'), conv_bias):
             if x is not None:
-                g['bias_' + n] = torch.empty_like(x)
+                g[n] = torch.empty_like(x)
     need = _lib.gdn2_prologue_bwd_workspace_bytes(B, T, N, H, HK, Dk, Dv, int(cu_seqlens is not None))
     if need == 0:
         raise Gdn2Error(GDN2_ERR_UNSUPPORTED, 'gdn2_prologue_bwd_workspace_bytes')
@@ -768,11 +773,9 @@ def prologue_bwd(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor, 
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f'workspace: must be contiguous on {dev}')
-    _call(_lib.gdn2_prologue_bwd, 'gdn2_prologue_bwd', dev, *(x.data_ptr() for x in raw), gates, ctypes.byref(sc),
-          _addr(slot_in), *(x.data_ptr() for x in grads),
-          *(g[n].data_ptr() for n in ('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit')),
-          *(g['weight_' + n].data_ptr() for n in 'qkv'), *(_addr(g.get('bias_' + n)) for n in 'qkv'),
-          _addr(cu_seqlens), B, T, N, H, HK, slots, Dk, Dv, _CODES[dt], _CODES[grad_dtype], workspace.data_ptr(),
+    _call(_lib.gdn2_prologue_bwd, 'gdn2_prologue_bwd', dev, *map(_data_ptr, raw), gates, ctypes.byref(sc),
+          _addr(slot_in), *map(_data_ptr, grads), *map(_data_ptr, outs), *map(_data_ptr, taps),
+          _addr(g.get('bias_q')), _addr(g.get('bias_k')), _addr(g.get('bias_v')), _addr(cu_seqlens), B, T, N, H, HK, slots, Dk, Dv, _CODES[dt], _CODES[grad_dtype], workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
     return g
 
@@ -791,7 +794,8 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     if x.dim() < 1 or shape[-1] < 1:
         raise ValueError('x must be [..., cols] with cols >= 1')
     cols = shape[-1]
-    _need(x, 'x', shape, dt, dev)
+    if not x.is_contiguous():
+        raise ValueError('x: must be contiguous')
     _need(weight, 'weight', (cols,), torch.float32, dev)
     if bias is not None:
         _need(bias, 'bias', (cols,), torch.float32, dev)
@@ -829,7 +833,8 @@ def layer_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, *, d
     rows = h.numel() // cols
     if dy.dtype not in _CODES:
         raise TypeError(f'unsupported gradient dtype {dy.dtype} (bfloat16 or float32)')
-    _need(h, 'h', shape, dt, dev)
+    if not h.is_contiguous():
+        raise ValueError('h: must be contiguous')
     _need(dy, 'dy', shape, dy.dtype, dev)
     _need(weight, 'weight', (cols,), torch.float32, dev)
     if dsum is not None:
