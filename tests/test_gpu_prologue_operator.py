@@ -304,3 +304,73 @@ def test_captured_and_replayed(T):
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, eo)) and all(torch.equal(x, y) for x, y in zip(hist, eh))
         assert all(torch.equal(g[n], eg[n]) for n in eg)
+
+
+@pytest.mark.parametrize('lens', [SHORT, LONG])
+def test_history_out_without_one_in(lens):
+    """No history in is zeros in, for sequences with and without tokens."""
+    N = len(lens)
+    p = Batch(15, lens, H=4, HK=2, dk=32, dv=64, slots=N + 2)
+    raw, weight, bias, hist, cu = p.gpu()
+    commit, slot = ints([i % 4 for i in range(N)]), ints(list(range(N))[::-1])
+    zeros, a, b = (tuple(f(h) for h in hist) for f in (torch.zeros_like, torch.clone, torch.clone))
+    x = gdn2.prologue_fwd(*raw, weight, bias, cu, conv_state=zeros, conv_state_out=a, slot_in=slot, commit=commit)
+    y = gdn2.prologue_fwd(*raw, weight, bias, cu, conv_state_out=b, slot_in=slot, commit=commit)
+    assert all(torch.equal(s, t) for s, t in zip(x, y)) and all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize('value', [float('nan'), float('inf')])
+def test_not_finite_stays_in_its_sequence(value):
+    """Three sequences in a few tiles, the middle one, its history and the rows behind the last one not finite:
+    the others' outputs, histories and gradients keep their bits."""
+    lens = [5, 6, 7]
+    p = Batch(16, lens, H=2, dk=64, dv=32, slots=4, tail=9)
+    raw, weight, bias, hist, cu = p.gpu()
+    grads = [torch.from_numpy(x).to(DEV).unsqueeze(0) for x in p.grads]
+    names = ('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit')
+
+    def run():
+        h = tuple(x.clone() for x in hist)
+        o = gdn2.prologue_fwd(*raw, weight, bias, cu, conv_state=h, conv_state_out=h, slot_in=slot)
+        g = gdn2.prologue_bwd(*raw, weight, bias, *grads, cu, conv_state=hist, slot_in=slot)
+        return [x.clone() for x in o] + [g[n] for n in names], h
+
+    slot = ints([2, 0, 1])
+    rows, pools = run()
+    for x in (*raw, *grads):
+        x[0, 5:11] = value
+        x[0, 18:] = value
+    for h in hist:
+        h[0] = value
+        h[3] = value
+    rows2, pools2 = run()
+    for x, y in zip(rows, rows2):
+        assert torch.equal(x[0, :5], y[0, :5]) and torch.equal(x[0, 11:18], y[0, 11:18])
+    for x, y in zip(pools, pools2):
+        assert torch.equal(x[1], y[1]) and torch.equal(x[2], y[2])
+    assert not torch.isfinite(rows2[0][0, 5:11]).all()
+
+
+def test_past_32_bit_offsets():
+    """Tokens behind 2^31 elements: the same bits as in a small call."""
+    n, heads, d = 70, 16, 128
+    T = (1 << 31) // (heads * d) + n + 9
+    p = Batch(17, [n], H=heads, dk=d, dv=d, gates='head')
+    raw, weight, bias, _, cu = p.gpu()
+    grads = [torch.from_numpy(x).to(DEV).unsqueeze(0) for x in p.grads]
+    small = gdn2.prologue_fwd(*raw, weight, bias, cu)
+    small_g = gdn2.prologue_bwd(*raw, weight, bias, *grads, cu)
+
+    def large(x):
+        y = torch.zeros((1, T, *x.shape[2:]), dtype=x.dtype, device=DEV)
+        y[:, -n:] = x
+        return y
+
+    cu2 = ints([0, T - n, T])
+    big = [large(x) for x in raw]
+    out = gdn2.prologue_fwd(*big, weight, bias, cu2)
+    assert all(torch.equal(x[:, -n:], y) for x, y in zip(out, small))
+    del out
+    g = gdn2.prologue_bwd(*big, weight, bias, *(large(x) for x in grads), cu2)
+    for m in ('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit'):
+        assert torch.equal(g[m][:, -n:], small_g[m]), m
