@@ -437,11 +437,26 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
         {
             const float m0 = sM[n][g], m1 = sM[n][g + 4];
             const bool query = n & 2;
-            f4 z = {0.f, 0.f, R[2], R[3]};
-            z = mfma4(query ? 0.f : m0, U[0] - R[0], z);
-            z = mfma4(query ? 0.f : m1, U[1] - R[1], z);
-            R = mfma4(query ? m0 : 0.f, z[0], z);
-            R = mfma4(query ? m1 : 0.f, z[1], R);
+            const float x0 = query ? 0.f : m0, x1 = query ? 0.f : m1, p0 = query ? m0 : 0.f, p1 = query ? m1 : 0.f;
+            const float u0 = U[0] - R[0], u1 = U[1] - R[1];
+            const f4 rq = {0.f, 0.f, R[2], R[3]};
+            const f4 z = mfma4(x1, u1, mfma4(x0, u0, rq));
+            R = mfma4(p1, z[1], mfma4(p0, z[0], z));
+            if (__builtin_amdgcn_ballot_w64(!(fabsf(z[0]) + fabsf(z[1]) < __builtin_inff()))) {
+                // Finite tokens whose product with the state is not: the zeros
+                // above a triangle must not meet it. One token after the other,
+                // from those up to it.
+                float d0 = 0.f, d1 = 0.f, o0 = 0.f, o1 = 0.f;
+                for (int t = 0; t < C; ++t) {
+                    const f4 y = mfma4(x1, g + 4 <= t ? u1 : 0.f, mfma4(x0, g <= t ? u0 : 0.f, rq));
+                    d0 = g == t ? y[0] : d0;
+                    d1 = g + 4 == t ? y[1] : d1;
+                    const f4 o = mfma4(p1, g + 4 <= t ? d1 : 0.f, mfma4(p0, g <= t ? d0 : 0.f, rq));
+                    o0 = g == t ? o[2] : o0;
+                    o1 = g + 4 == t ? o[3] : o1;
+                }
+                R = (f4){g < stay ? d0 : 0.f, g + 4 < stay ? d1 : 0.f, o0, o1};
+            }
         }
         if (stay > 0)
 #pragma unroll

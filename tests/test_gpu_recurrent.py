@@ -202,6 +202,28 @@ def test_not_finite_reaches_no_earlier_token(name, value):
     assert not np.all(np.isfinite(o1[at, 1]))
 
 
+@pytest.mark.parametrize('dtype', ['bf16', 'f32'])
+@pytest.mark.parametrize('at', [1, 4, 5, 7])
+@pytest.mark.parametrize('d', [32, 128])
+def test_overflow_reaches_no_earlier_token(d, at, dtype):
+    """A finite token whose product with the state overflows: the tokens before it in its block and the prefix
+    kept without it keep their bits."""
+    lens = [3, 8, 8]
+    kept = min(at, 4)
+
+    def one(k):
+        p = Batch(14, lens, H=2, dk=d, dv=d, dtype=dtype)
+        p.state[1:] *= np.float32(1e20)
+        p.k[3 + at, 1] *= k
+        return run(p, commit=[3, kept, 8])
+
+    o0, s0 = one(np.float32(1))
+    o1, s1 = one(np.float32(2.0 ** 70))
+    assert np.all(np.isfinite(o0)) and not np.all(np.isfinite(o1[3 + at, 1]))
+    assert np.array_equal(o0[:3 + at], o1[:3 + at]) and np.array_equal(o0[11:], o1[11:])
+    assert np.array_equal(o0[:, 0], o1[:, 0]) and np.array_equal(s0, s1) and np.all(np.isfinite(s1))
+
+
 def test_matches_decode_step():
     """Tokens one by one through gdn2_decode_step give the same outputs and states."""
     p = Batch(14, [5] * 3, H=4, dk=128, dv=128)
