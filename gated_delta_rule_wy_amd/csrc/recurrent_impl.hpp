@@ -205,6 +205,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
 #pragma unroll
             for (int j = 0; j < 4; ++j) sp[(16 * r + j) * DV] = S[r][j];
     };
+    // sum over the four rows of 16 lanes
+    auto across = [](float v) {
+        const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+        const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    };
     // row `row` (of lane n) of sX times the state, in two chains of products
     auto left_product = [&](int row) {
         f4 R[2] = {f4zero(), f4zero()};
@@ -258,7 +265,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
     //    draft's end (its committed part stays one block), then token by token;
     //  - a channel decays by more than 2^60 within it: A and P are formed as
     //    products of rows decayed from the block's start and keys divided by
-    //    that decay. Half the tokens, down to one, which needs neither.
+    //    that decay (nor may a key overflow by it). Half the tokens, down to
+    //    one, which needs neither.
     int most = C, L = 0, par = 0;
     // A block ends at the committed prefix, whose state is kept, but for the
     // last one, whose later tokens then leave the state alone.
@@ -336,11 +344,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
             }
             scan(dd, up, on, all, lane);
             f4 ki;
-            wide = wide || !(fminf(fminf(up[0], up[1]), fminf(up[2], up[3])) >= 0x1p-60f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 ki[e] = L > 1 ? kk[e] * __builtin_amdgcn_rcpf(up[e]) : kk[e];
             }
+            wide = wide || !(fminf(fminf(up[0], up[1]), fminf(up[2], up[3])) >= 0x1p-60f) ||
+                   !(fabsf(ki[0]) + fabsf(ki[1]) + fabsf(ki[2]) + fabsf(ki[3]) < __builtin_inff());
             if (stay < L) {
                 f4 none;
 #pragma unroll
@@ -443,14 +452,23 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
             const f4 z = mfma4(x1, u1, mfma4(x0, u0, rq));
             R = mfma4(p1, z[1], mfma4(p0, z[0], z));
             if (__builtin_amdgcn_ballot_w64(!(fabsf(z[0]) + fabsf(z[1]) < __builtin_inff()))) {
-                // Finite tokens whose product with the state is not: the zeros
-                // above a triangle must not meet it. One token after the other,
-                // from those up to it.
+                // Finite tokens whose product with the state, or whose X, is
+                // not: the zeros above a triangle must not meet it. One token
+                // after the other, from those up to it: as above, and by A
+                // itself where X fails.
                 float d0 = 0.f, d1 = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll 1
                 for (int t = 0; t < C; ++t) {
+                    float a0 = 0.f, a1 = 0.f;   // A of token t with tokens g and g + 4
+#pragma unroll 1
+                    for (int z = 0; z < NAP; ++z) {
+                        a0 += sPart[z][t & 3][g][t >> 2];
+                        a1 += sPart[z][t & 3][g + 4][t >> 2];
+                    }
+                    const float e = across((g < t ? a0 * d0 : 0.f) + (g + 4 < t ? a1 * d1 : 0.f));
                     const f4 y = mfma4(x1, g + 4 <= t ? u1 : 0.f, mfma4(x0, g <= t ? u0 : 0.f, rq));
-                    d0 = g == t ? y[0] : d0;
-                    d1 = g + 4 == t ? y[1] : d1;
+                    d0 = g == t ? (fabsf(y[0]) < __builtin_inff() ? y[0] : u0 - e) : d0;
+                    d1 = g + 4 == t ? (fabsf(y[1]) < __builtin_inff() ? y[1] : u1 - e) : d1;
                     const f4 o = mfma4(p1, g + 4 <= t ? d1 : 0.f, mfma4(p0, g <= t ? d0 : 0.f, rq));
                     o0 = g == t ? o[2] : o0;
                     o1 = g + 4 == t ? o[3] : o1;

@@ -202,6 +202,15 @@ def test_not_finite_reaches_no_earlier_token(name, value):
     assert not np.all(np.isfinite(o1[at, 1]))
 
 
+def test_large_keys_under_strong_decay():
+    """A key that overflows when it is divided by its block's decay, and does not by itself."""
+    p = Batch(16, [8, 3, 8], H=2, dk=32, dv=32, dtype='f32', decay=-5.0)   # down to 2^-58 over a block
+    p.k[6, 0, :4] *= np.float32(1e25)   # over a decay of e^-35: past the largest float
+    p.state[0] *= np.float32(1e-20)   # (what the key meets stays small)
+    p.v *= np.float32(1e-10)
+    check(p, 'large key')
+
+
 @pytest.mark.parametrize('dtype', ['bf16', 'f32'])
 @pytest.mark.parametrize('at', [1, 4, 5, 7])
 @pytest.mark.parametrize('d', [32, 128])
