@@ -671,6 +671,8 @@ def _conv_pools(conv_weight, conv_bias, conv_state, conv_state_out, heads, dims,
         _need(t, 'conv_weight', (h * d, 4), f32, dev)
         addr[z] = t.data_ptr()
     if conv_bias is not None:
+        if len(conv_bias) != 3:
+            raise ValueError('conv_bias must be a (q, k, v) triple')
         for z, (t, h, d) in enumerate(zip(conv_bias, heads, dims)):
             if t is not None:
                 _need(t, 'conv_bias', (h * d,), f32, dev)

@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <vector>
 
 namespace {
@@ -481,6 +482,15 @@ int gdn2_decode_step_prologue(const void *q_raw, const void *k_raw, const void *
 
 static bool dtype_ok(int t) { return t == GDN2_F32 || t == GDN2_BF16; }
 
+// Whether an output is an input's own memory (partial overlaps are the caller's).
+static bool same_memory(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins)
+{
+    for (const void *o : outs)
+        for (const void *i : ins)
+            if (o && o == i) return true;
+    return false;
+}
+
 // Sizes shared by the recurrence on slots and the prologue.
 static int serve_check(int B, int T, int N, int H, int HK, int dk, int dv, int in_dtype, int varlen)
 {
@@ -511,6 +521,7 @@ int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float 
     const void *ptrs[] = {q, k, v, log_alpha, b, w, state, slot_in, slot_out, commit, o, cu_seqlens};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
+    if (same_memory({o}, {q, k, v, log_alpha, b, w, state})) return GDN2_ERR_INVALID;
     gdn2::RecurrentArgs a;
     a.q = q; a.k = k; a.v = v; a.b = b; a.w = w;
     a.log_alpha = log_alpha;
@@ -583,6 +594,8 @@ int gdn2_prologue_fwd(const void *q_raw, const void *k_raw, const void *v_raw, c
     const void *ptrs[] = {q, k, v, b, w, slot_out, commit};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
+    if (same_memory({q, k, v}, {q_raw, k_raw, v_raw, b_logit, w_logit}) || same_memory({b, w}, {q_raw, k_raw, v_raw}))
+        return GDN2_ERR_INVALID;
     a.y[0] = q; a.y[1] = k; a.y[2] = v;
     a.gate[0] = b; a.gate[1] = w;
     a.slot_out = slot_out;
@@ -620,6 +633,9 @@ int gdn2_prologue_bwd(const void *q_raw, const void *k_raw, const void *v_raw, c
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
     if (!workspace || workspace_bytes < gdn2_prologue_bwd_workspace_bytes(B, T, N, H, HK, dk, dv, cu_seqlens != nullptr))
         return GDN2_ERR_WORKSPACE;
+    if (same_memory({dq_raw, dk_raw, dv_raw, db_logit, dw_logit},
+                    {q_raw, k_raw, v_raw, b_logit, w_logit, dq, dk_, dv_, db, dw}))
+        return GDN2_ERR_INVALID;
     a.dy[0] = dq; a.dy[1] = dk_; a.dy[2] = dv_;
     a.dgate[0] = db; a.dgate[1] = dw;
     a.dx[0] = dq_raw; a.dx[1] = dk_raw; a.dx[2] = dv_raw;

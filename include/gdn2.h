@@ -391,7 +391,7 @@ int gdn2_chunk_bwd_kept(const void *q, const void *k, const void *v, const float
  * sequence, never an earlier token or a prefix kept without it.
  *
  * dk, dv in {16, 32, 64, 128}. GDN2_ERR_INVALID also for HK not dividing H,
- * slots < 1, or slot_in NULL with slots < N.
+ * slots < 1, slot_in NULL with slots < N, or an output that is an input.
  */
 int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float *log_alpha, const void *b,
                        const void *w, int gates, float *state, const int32_t *slot_in, const int32_t *slot_out,

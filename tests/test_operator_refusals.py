@@ -135,6 +135,31 @@ def test_layer_norm_workspace():
     assert W(1 << 30, 2048) <= 64 << 20
 
 
+@pytest.mark.parametrize('name', ['q', 'k', 'v', 'la', 'b', 'w', 'state'])
+def test_recurrent_rejects_an_output_that_is_an_input(name):
+    ins = {n: (i + 2) * P for i, n in enumerate(('q', 'k', 'v', 'la', 'b', 'w', 'state'))}
+    assert recurrent(**ins, o=ins[name]) == INVALID
+
+
+@pytest.mark.parametrize('out', ['yq', 'yk', 'yv', 'yb', 'yw'])
+@pytest.mark.parametrize('name', ['q', 'k', 'v', 'xb', 'xw'])
+def test_prologue_fwd_rejects_an_output_that_is_an_input(out, name):
+    if out in ('yb', 'yw') and name in ('xb', 'xw'):
+        return   # (gates in place of their logits are allowed)
+    at = {n: (i + 2) * P for i, n in enumerate(('q', 'k', 'v', 'xb', 'xw', 'yq', 'yk', 'yv', 'yb', 'yw'))}
+    at[out] = at[name]
+    assert prologue_fwd(**at) == INVALID
+
+
+@pytest.mark.parametrize('out', ['gq', 'gk', 'gv', 'gb', 'gw'])
+@pytest.mark.parametrize('name', ['q', 'k', 'v', 'xb', 'xw', 'dq', 'dk_', 'dv_', 'db', 'dw'])
+def test_prologue_bwd_rejects_an_output_that_is_an_input(out, name):
+    at = {n: (i + 2) * P for i, n in enumerate(('q', 'k', 'v', 'xb', 'xw', 'dq', 'dk_', 'dv_', 'db', 'dw', 'gq', 'gk',
+                                                'gv', 'gb', 'gw'))}
+    at[out] = at[name]
+    assert prologue_bwd(**at) == INVALID
+
+
 # ---- the Python binding: wrong shapes, types and devices raise before the library is called
 
 def _mix(B=1, T=4, H=2, HK=2, dk=32, dv=32, dt=torch.bfloat16):
@@ -197,7 +222,7 @@ def test_recurrent_binding_refuses(change):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize('change', ['weight shape', 'weight count', 'bias dtype', 'pool dtype', 'pool slots', 'slots',
+@pytest.mark.parametrize('change', ['weight shape', 'weight count', 'bias count', 'bias dtype', 'pool dtype', 'pool slots', 'slots',
                                     'logit shape', 'out count', 'out shape', 'grad shape', 'grad dtype'])
 def test_prologue_binding_refuses(change):
     dev = torch.device('cuda:0')
@@ -207,6 +232,7 @@ def test_prologue_binding_refuses(change):
     kw, cu = dict(conv_state=pool), None
     if change == 'weight shape': wt = (wt[0], wt[1][:32].contiguous(), wt[2])   # noqa: E701
     if change == 'weight count': wt = wt[:2]   # noqa: E701
+    if change == 'bias count': bs = bs[:2]   # noqa: E701
     if change == 'bias dtype': bs = tuple(x.bfloat16() for x in bs)   # noqa: E701
     if change == 'pool dtype': kw['conv_state'] = tuple(x.float() for x in pool)   # noqa: E701
     if change == 'pool slots': kw['conv_state'] = (pool[0], pool[1], pool[2][:1].contiguous())   # noqa: E701
