@@ -665,6 +665,9 @@ int gdn2_layer_norm_fwd(const void *x, const void *residual, const float *weight
     const void *ptrs[] = {x, residual, weight, bias, y, sum};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
+    // (in place only where the elements have one size; weights are never outputs)
+    if (in_dtype != out_dtype && same_memory({y}, {x, residual})) return GDN2_ERR_INVALID;
+    if (same_memory({y, sum}, {weight, bias})) return GDN2_ERR_INVALID;
     gdn2::LayerNormArgs a;
     a.x = x;
     a.residual = residual;
@@ -699,6 +702,9 @@ int gdn2_layer_norm_bwd(const void *dy, const void *h, const float *weight, cons
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
     if (!workspace || workspace_bytes < gdn2_layer_norm_bwd_workspace_bytes(rows, cols)) return GDN2_ERR_WORKSPACE;
+    if (in_dtype != out_dtype && same_memory({dh}, {dy})) return GDN2_ERR_INVALID;
+    if (same_memory({dh, dweight, dbias}, {weight}) || same_memory({dweight, dbias}, {dy, h, dsum, dh}))
+        return GDN2_ERR_INVALID;
     gdn2::LayerNormBwdArgs a;
     a.dy = dy;
     a.h = h;

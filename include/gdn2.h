@@ -464,8 +464,8 @@ int gdn2_prologue_bwd(const void *q_raw, const void *k_raw, const void *v_raw, c
  *   y            [rows, cols] out_dtype
  *   sum          [rows, cols] in_dtype, or NULL: receives h, rounded
  * y and sum may each be x or residual itself (same type), but must not overlap
- * an input otherwise, nor each other (y == sum: GDN2_ERR_INVALID). mean and variance are those of the
- * unrounded h, in fp32.
+ * an input otherwise, nor each other (GDN2_ERR_INVALID where they are one).
+ * mean and variance are those of the unrounded h, in fp32.
  *
  * gdn2_layer_norm_bwd: from dy = dL/dy (out_dtype of the forward) and h (the
  * sum the forward wrote, or its x; in_dtype), dh = dL/dh (in_dtype; the

@@ -128,6 +128,16 @@ def test_layer_norm_bwd_rejects(kw, status):
     assert layer_norm_bwd(**kw) == status
 
 
+def test_layer_norm_rejects_outputs_over_inputs():
+    """In place is for one type: y over x or the residual, dh over dy; never over a weight."""
+    at = dict(x=2 * P, res=3 * P, w=4 * P, b=5 * P, y=6 * P, s=7 * P)
+    for kw in (dict(y=2 * P), dict(y=3 * P), dict(y=4 * P, odt=BF16), dict(s=5 * P)):
+        assert layer_norm_fwd(**{**at, **kw}) == INVALID, kw
+    at = dict(dy=2 * P, h=3 * P, w=4 * P, ds=5 * P, dh=6 * P, dw=7 * P, db=8 * P)
+    for kw in (dict(dh=2 * P), dict(dh=4 * P), dict(dw=4 * P), dict(db=2 * P), dict(dw=6 * P)):
+        assert layer_norm_bwd(**{**at, **kw}) == INVALID, kw
+
+
 def test_layer_norm_workspace():
     W = lib.gdn2_layer_norm_bwd_workspace_bytes
     assert W(0, 64) > 0 and W(1 << 30, 1 << 20) > 0
