@@ -16,7 +16,10 @@
 // -inf (a full forget); the quotients need D_s >= 2^-60 (the
 // products then stay far from the smallest floats), and a block with less is
 // cut in half, down to a single token, which has none. All of it is
-// fp32, the products on the fp32 matrix instruction.
+// fp32, the products on the fp32 matrix instruction. Products with the zeros
+// above a triangle are harmless but for values that are not finite: blocks
+// with such tokens are cut, and products that overflow are formed anew, a
+// token at a time.
 //
 // A workgroup of dv/16 waves (or half as many) owns the state of one (sequence,
 // head), or half its columns, a wave 16 of them in registers: tile r, lane n + 16g holds rows 16r + 4g + j of
