@@ -380,6 +380,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
         if (bad != 0.f) sFlag[par].x = 1;   // (0 x: NaN unless x is finite)
         if (wide) sFlag[par].y = 1;
         __syncthreads();
+        // ---- A and P: the decayed rows by the keys over their decays (their
+        // fragments first: what follows takes as long as they do to arrive)
+        constexpr int NT_AP = (NR + NAP - 1) / NAP;
+        f4 fx[NT_AP], fk[NT_AP];
+        if (NAP == NW || wv < NAP) {
+#pragma unroll
+            for (int m = 0; m < NT_AP; ++m) {
+                const int at = 16 * (m * NAP + wv) + 4 * g;
+                fx[m] = *reinterpret_cast<const f4 *>(&sX[n][at]);
+                fk[m] = *reinterpret_cast<const f4 *>(&sKi[n & 7][at]);
+            }
+        }
         // (one value for all: the block's bounds stay in scalar registers)
         const int bads = __builtin_amdgcn_readfirstlane(sFlag[par].x), wides = __builtin_amdgcn_readfirstlane(sFlag[par].y);
         if (L > 1 && (bads | wides)) {
@@ -392,24 +404,19 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
             continue;
         }
         if (tid == 0) sFlag[par ^ 1] = make_int2(0, 0);
+        // lane n (of 8) + 16 g has A and P of tokens g and g + 4 with token n
+        f4 ap = f4zero();
+        if (NAP == NW || wv < NAP) {
+#pragma unroll
+            for (int m = 0; m < NT_AP; ++m) ap = Mma<float>::mma(fx[m], fk[m], ap);
+        }
         // the next block's loads, under way during this one's products
         const int next = done + L, Lb = L;
         if (next < len) {
             L = length(next);
             load_block(t0 + next, L, lane);
         }
-
-        // ---- A and P: the decayed rows by the keys over their decays; lane n
-        // (of 8) + 16 g has A and P of tokens g and g + 4 with token n
-        if (NAP == NW || wv < NAP) {
-            f4 ap = f4zero();
-#pragma unroll
-            for (int r0 = 0; r0 < NR; r0 += NAP) {
-                const int at = 16 * (r0 + wv) + 4 * g;
-                ap = Mma<float>::mma(*reinterpret_cast<const f4 *>(&sX[n][at]), *reinterpret_cast<const f4 *>(&sKi[n & 7][at]), ap);
-            }
-            if (n < C) *reinterpret_cast<f4 *>(&sPart[wv][g][n][0]) = ap;
-        }
+        if ((NAP == NW || wv < NAP) && n < C) *reinterpret_cast<f4 *>(&sPart[wv][g][n][0]) = ap;
         __syncthreads();
 
         // ---- X and P by wave 0 (X a column a lane, the entries of A as
@@ -437,12 +444,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
             if (Lb == 1) sM[rec_row(0) + 2][0] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ap[2]), 16));
         }
         f4 R = left_product(n);
-        // the state's decay, while wave 0 works
-        if (stay > 0)
+        // the state's decay, while wave 0 works (by one where nothing stays)
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                S[r] *= *reinterpret_cast<const f4 *>(&sG[par][16 * r + 4 * g]);
-            }
+        for (int r = 0; r < NR; ++r) S[r] *= *reinterpret_cast<const f4 *>(&sG[par][16 * r + 4 * g]);
         __syncthreads();
 
         // ---- Delta = X (U - R_E), O = R_Q + P Delta, then the state
