@@ -11,7 +11,7 @@
 //   A_ts = (b_t k_t D_t) . (k_s / D_s)  (t > s),  P_ts = (q_t D_t) . (k_s / D_s)  (t >= s)
 //   R_E = (b k D) S0, R_Q = (q D) S0, X = (I + A)^-1
 //   Delta = X (U - R_E),  O = R_Q + P Delta
-//   S = D_8 S0 + (k alpha_{t+1} .. alpha_8)^T Delta
+//   S = D_8 S0 + (k_t D_8 / D_t)^T Delta
 // Decays are running products of alphas, so log alpha may be anything down to
 // -inf (a full forget); the quotients need D_s >= 2^-60 (the
 // products then stay far from the smallest floats), and a block with less is
@@ -22,9 +22,10 @@
 // token at a time.
 //
 // A workgroup of dv/16 waves (or half as many) owns the state of one (sequence,
-// head), or half its columns, a wave 16 of them in registers: tile r, lane n + 16g holds rows 16r + 4g + j of
-// column n, which is the accumulator layout, and with element j of a 16-deep
-// fragment on row 4g + j also the right operand's. The block's 16 left rows are
+// head), or half its columns, a wave 16 of them in registers: tile r, lane n +
+// 16g holds rows 16r + 4g + j of column n, which is the accumulator layout, and
+// with element j of a 16-deep fragment on row 4g + j also the right operand's.
+// The block's 16 left rows are
 // ordered so that rows 4g .. 4g+3 are the erase rows of tokens g and g+4 and
 // their query rows: the first product leaves in each lane just what the second
 // one (by X, then P,) takes as its right operand, which leaves Delta where the
@@ -35,10 +36,12 @@
 // Measured at 128 x 128 heads (bf16 inputs): 256 sequences x 16 heads, one
 // token, 110 us (4.9 TB/s; the same bytes multiplied in place by a library
 // kernel 91 us); 128 sequences x 32 heads of 0 to 8 tokens, part committed,
-// 89 us (5.4 TB/s). With more tokens a sequence the blocks come one after the
-// other: about 2.7 us a block of one chain alone, of which the products are 1800
-// cycles of 6300; 48 sequences x 16 heads of up to 64 fp32 tokens (128 x 64)
-// take 43 us, a third of them at the matrix cores' rate.
+// 90 us (5.4 TB/s). With more tokens a sequence the blocks come one after the
+// other: about 2.6 us a block of one chain alone, some 6500 cycles, of which
+// a quarter prepares the rows, an eighth forms X in one wave, and the matrix
+// products need 1900; 256 x 16 chains of 64 tokens 407 us; 48 sequences x 16
+// heads of up to 64 fp32 tokens (128 x 64) 42 us, a third of them at the matrix
+// cores' rate.
 #pragma once
 
 #include "gdn2_launch.hpp"
@@ -289,27 +292,23 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
         for (int j = 0; j < 2; ++j) load_u(tb, min((lane >> 4) + 4 * j, L - 1), col0 + 16 * wv + (lane & 15), cu[j]);
     };
     // Of the products of d over a channel's 8 tokens (lanes 8 apart): up to the
-    // lane's token, behind it, and of all. Each step joins the groups of
-    // tokens that differ in one bit.
-    auto scan = [&](const f4 &d, f4 &up, f4 &behind, f4 &all, int lane) {
+    // lane's token, and of all. Each step joins the groups of tokens that
+    // differ in one bit.
+    auto scan = [&](const f4 &d, f4 &up, f4 &all, int lane) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float p = d[e], q = 1.f, t = d[e];
+            float p = d[e], t = d[e];
             const float o8 = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(t), 0x128, 0xF, 0xF, false));   // row_ror:8
             p *= lane & 8 ? o8 : 1.f;
-            q *= lane & 8 ? 1.f : o8;
             t *= o8;
             const auto a16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(t), __float_as_uint(t), false, false);
             const float e16 = __uint_as_float(a16[0]), f16 = __uint_as_float(a16[1]);   // of the even row, of the odd one
             p *= lane & 16 ? e16 : 1.f;
-            q *= lane & 16 ? 1.f : f16;
             t = e16 * f16;
             const auto a32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(t), __float_as_uint(t), false, false);
             const float e32 = __uint_as_float(a32[0]), f32 = __uint_as_float(a32[1]);
             p *= lane & 32 ? e32 : 1.f;
-            q *= lane & 32 ? 1.f : f32;
             up[e] = p;
-            behind[e] = q;
             all[e] = e32 * f32;
         }
     };
@@ -337,30 +336,36 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
             make_item(x[m], kk, qq, bb, dd);
             // (a token alone: its query, undecayed, in the next one's row too, for q.k)
             const bool alone = L == 1 && t == 1;
+            if (L < C)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                kk[e] = t < L ? kk[e] : 0.f;
-                qq[e] = t < L || alone ? qq[e] : 0.f;
-                bb[e] = t < L ? bb[e] : 0.f;
-                dd[e] = t < L ? dd[e] : 1.f;
-                bad += 0.f * (kk[e] + qq[e] + bb[e] + dd[e]);
-            }
-            scan(dd, up, on, all, lane);
+                for (int e = 0; e < 4; ++e) {
+                    kk[e] = t < L ? kk[e] : 0.f;
+                    qq[e] = t < L || alone ? qq[e] : 0.f;
+                    bb[e] = t < L ? bb[e] : 0.f;
+                    dd[e] = t < L ? dd[e] : 1.f;
+                }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad += 0.f * (kk[e] + qq[e] + bb[e] + dd[e]);
+            scan(dd, up, all, lane);
             f4 ki;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                ki[e] = L > 1 ? kk[e] * __builtin_amdgcn_rcpf(up[e]) : kk[e];
+                const float r = __builtin_amdgcn_rcpf(up[e]);
+                ki[e] = L > 1 ? kk[e] * r : kk[e];
+                on[e] = L > 1 ? all[e] * r : 1.f;   // what decays behind the token
             }
             wide = wide || !(fminf(fminf(up[0], up[1]), fminf(up[2], up[3])) >= 0x1p-60f) ||
                    !(fabsf(ki[0]) + fabsf(ki[1]) + fabsf(ki[2]) + fabsf(ki[3]) < __builtin_inff());
             if (stay < L) {
-                f4 none;
+                f4 part;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     kk[e] = t < stay ? kk[e] : 0.f;
                     dd[e] = t < stay ? dd[e] : 1.f;
                 }
-                scan(dd, none, on, all, lane);
+                scan(dd, part, all, lane);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) on[e] = L > 1 ? all[e] * __builtin_amdgcn_rcpf(part[e]) : 1.f;
             }
             if (DK >= 32 || c < DK) {
                 *reinterpret_cast<f4 *>(&sX[rec_row(t)][c]) = bb * up;
