@@ -275,7 +275,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
     //    one, which needs neither.
     int most = C, L = 0, par = 0;
     // A block ends at the committed prefix, whose state is kept, but for the
-    // last one, whose later tokens then leave the state alone.
+    // last one, whose later tokens then leave the state alone. (Also one that
+    // was cut: it may no longer be the last.)
     auto length = [&](int done) {
         const int rem = len - done;
         return rem <= most ? rem : min(most, done < commit ? commit - done : rem);
@@ -400,9 +401,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 1
         // (one value for all: the block's bounds stay in scalar registers)
         const int bads = __builtin_amdgcn_readfirstlane(sFlag[par].x), wides = __builtin_amdgcn_readfirstlane(sFlag[par].y);
         if (L > 1 && (bads | wides)) {
-            if (!bads) most = L = L / 2;
-            else if (done < commit && commit < done + L) L = commit - done;
-            else most = L = 1;
+            if (!bads) {
+                most = L / 2;
+                L = length(done);
+            } else if (done < commit && commit < done + L) {
+                L = commit - done;
+            } else {
+                most = L = 1;
+            }
             load_block(tb, L, lane);
             if (tid == 0) sFlag[par ^ 1] = make_int2(0, 0);
             __syncthreads();

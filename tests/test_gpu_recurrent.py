@@ -348,3 +348,53 @@ def test_two_streams_share_a_pool():
         (o_ref, s_ref) = p.reference(slot_in=at)
         ref.check(f'o {name}', outs[name][0].cpu().numpy(), o_ref)
         ref.check(f'state {name}', state.cpu().numpy()[at], (s_ref[0][at], s_ref[1][at]))
+
+
+def _cut(pairs, d, dtype, moved, decay=None, gates='channel'):
+    """A draft of n tokens with c kept for each (n, c) of ``pairs``, in scattered slots; moved: into other ones."""
+    N = len(pairs)
+    perm = np.random.default_rng(N).permutation(2 * N + 1)
+    p = Batch(23, [n for n, _ in pairs], H=2, dk=d, dv=d, dtype=dtype, gates=gates, slots=2 * N + 1, decay=decay)
+    kw = dict(slot_in=perm[:N].tolist(), commit=[c for _, c in pairs])
+    if moved:
+        kw['slot_out'] = perm[N:2 * N].tolist()
+    return p, kw
+
+
+@pytest.mark.parametrize('moved', [False, True])
+@pytest.mark.parametrize('decay', [-5.5, -6.0, -12.0, -30.0, float('-inf')])
+@pytest.mark.parametrize('d,dtype,gates,top', [(32, 'f32', 'channel', 17), (64, 'bf16', 'head', 17), (128, 'bf16', 'channel', 9)])
+def test_commit_in_a_block_cut_for_its_decay(d, dtype, gates, top, decay, moved):
+    """Every commit of every length around one and two blocks, with decays that cut them."""
+    p, kw = _cut([(n, c) for n in range(2, top + 1) for c in range(n + 1)], d, dtype, moved, decay, gates)
+    with np.errstate(divide='ignore', invalid='ignore'):
+        check(p, f'commit under {decay}', **kw)
+
+
+@pytest.mark.parametrize('decay', [-6.0, -12.0])
+def test_commit_in_a_cut_block_of_few_chains(decay):
+    """The same where two workgroups share a chain."""
+    p, kw = _cut([(8, c) for c in range(9)], 128, 'bf16', False, decay)
+    check(p, f'few chains {decay}', **kw)
+
+
+@pytest.mark.parametrize('moved', [False, True])
+@pytest.mark.parametrize('channels', [slice(3, 4), slice(None)])
+@pytest.mark.parametrize('n', [2, 3, 4, 5, 6, 7, 8, 9, 12, 16, 17])
+def test_commit_around_a_full_forget(n, channels, moved):
+    """One token that forgets a channel, or all, at each place before and behind each commit."""
+    at = [t for t in range(n) for _ in range(n + 1)]
+    p, kw = _cut([(n, i % (n + 1)) for i in range(n * (n + 1))], 32, 'f32', moved)
+    for i, t in enumerate(at):
+        p.la[i * n + t, :, channels] = -np.inf
+    with np.errstate(divide='ignore', invalid='ignore'):
+        check(p, f'forget in {n}', **kw)
+
+
+def test_commit_where_only_the_last_block_is_cut():
+    """Mild decay up to the sequence's last block, which decays by more than 2^60."""
+    pairs = [(n, c) for n in range(9, 25) for c in range(n + 1)]
+    p, kw = _cut(pairs, 32, 'f32', True)
+    for end, n in zip(p.cu[1:], p.lens):
+        p.la[end - ((n - 1) % 8 + 1):end] = -9
+    check(p, 'last block', **kw)
