@@ -52,6 +52,10 @@ __device__ __forceinline__ float head_sum(float x, int G)
     return x;
 }
 
+// 1 / max(|y|, 1e-12) from the sum of squares, NaN where that is NaN (which a
+// maximum would replace by the floor).
+__device__ __forceinline__ float unit_scale(float ss) { return rsqrtf(ss < 1e-24f ? 1e-24f : ss); }
+
 struct SeqTable {
     const int32_t *cu;   // or null: sequences of T tokens
     int T, N;            // T: tokens of a sequence, or in all
@@ -366,7 +370,7 @@ __global__ __launch_bounds__(kNT) void prologue_fwd_kernel(ProParams p)
                     old[2][c] = now;
                 }
                 if (z < 2) {
-                    const float r = rsqrtf(fmaxf(head_sum(ss, G), 1e-24f));
+                    const float r = unit_scale(head_sum(ss, G));
 #pragma unroll
                     for (int c = 0; c < V; ++c) o[c] *= r;
                 }
@@ -535,9 +539,9 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
                         }
                         ss = head_sum(ss, G);
                         yd = head_sum(yd, G);
-                        const float r = rsqrtf(fmaxf(ss, 1e-24f));
+                        const float r = unit_scale(ss);
                         // (r y).dq along the unit vector; none where the norm is at its floor
-                        const float m = ss > 1e-24f ? r * yd * r : 0.f;
+                        const float m = ss <= 1e-24f ? 0.f : r * yd * r;
 #pragma unroll
                         for (int c = 0; c < V; ++c) d[c] = r * (d[c] - m * y[c]);
                     }

@@ -374,3 +374,34 @@ def test_past_32_bit_offsets():
     g = gdn2.prologue_bwd(*big, weight, bias, *(large(x) for x in grads), cu2)
     for m in ('q_raw', 'k_raw', 'v_raw', 'b_logit', 'w_logit'):
         assert torch.equal(g[m][:, -n:], small_g[m]), m
+
+
+@pytest.mark.parametrize('value', [float('nan'), float('inf')])
+@pytest.mark.parametrize('dtype', ['bf16', 'f32'])
+@pytest.mark.parametrize('lens', [[7, 9], [30, 41]])
+@pytest.mark.parametrize('d', [16, 128])
+def test_one_channel_not_finite(d, lens, dtype, value):
+    """One channel of one token: NaN wherever the formulas have it (the head's other channels, whose norm it is
+    part of, and their gradients), the formulas' values everywhere else."""
+    p = Batch(18, lens, H=2, dk=d, dv=d, dtype=dtype)
+    n, at = sum(lens), lens[0] + 3
+    for x in p.raw:
+        x[at, 1, 5] = value
+    print(f'[one channel] d={d} lens={lens} {dtype} {value}', flush=True)
+    raw, weight, bias, _, cu = p.gpu()
+    out = gdn2.prologue_fwd(*raw, weight, bias, cu)
+    grads = [torch.from_numpy(x).to(DEV).unsqueeze(0) for x in p.grads]
+    g = gdn2.prologue_bwd(*raw, weight, bias, *grads, cu)
+    with np.errstate(all='ignore'):
+        want, _ = ref.prologue_fwd(p.raw, p.logits, p.weight, p.bias, lens, dtype=dtype)
+        wantg = ref.prologue_bwd(p.raw, p.logits, p.weight, p.bias, p.grads, lens, dtype=dtype)
+    pairs = [(m, back(x)[0, :n], y) for m, x, y in zip(NAMES, out, want)]
+    pairs += [(m, back(g[m])[0, :n] if m.endswith(('raw', 'logit')) else back(g[m]), wantg[m]) for m in wantg]
+    for m, x, (y, tol) in pairs:
+        x = x.reshape(y.shape)
+        assert np.array_equal(np.isnan(x), np.isnan(y)), f'{m}: NaN in {np.isnan(x).sum()} places, not {np.isnan(y).sum()}'
+        fin = np.isfinite(y)
+        assert np.array_equal(x[~fin & ~np.isnan(y)], y[~fin & ~np.isnan(y)]), m
+        # (no tolerance, NaN, at the zeros that dividing by an infinite norm leaves: those are exact)
+        ref.check(m, x[fin], (y[fin], np.nan_to_num(tol[fin])))
+    assert value == value or (np.isnan(want[0][0][at, 1]).all() and np.isnan(wantg['bias_q'][0].reshape(2, d)[1]).all())
