@@ -7,7 +7,7 @@
 //   gate = 1 / (1 + exp(-logit))
 //   backward: dy = dq (v), dy = r dq - y r^3 (y.dq) (q, k; r dq where |y| <= 1e-12)
 //     dx_t = sum_j w_j dy_{t+3-j},  dw_j = sum_t dy_t x_{t-3+j},  dbias = sum_t dy_t
-//     dlogit = dgate s (1 - s)
+//     dlogit = dgate s (1 - s) = dgate e / (1 + e)^2,  e = exp(-|logit|)
 //
 // Bound by memory: every element is read once and written once. A thread owns
 // a few neighbouring channels of one tensor (the lanes of a head are
@@ -418,9 +418,11 @@ __device__ void gate_bwd(const ProGate &gt, int64_t total, int block)
     const In *x = (const In *)gt.x + at;
     const float *dy = gt.dy + at;
     Out *dx = (Out *)gt.y + at;
+    // s (1 - s), with no difference of s from one to take: exact to a few units
+    // also where s rounds to one
     auto one = [](float z, float d) {
-        const float s = __builtin_amdgcn_rcpf(1.f + __expf(-z));
-        return d * s * (1.f - s);
+        const float e = __expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + e);
+        return d * e * (r * r);
     };
     if (at + 8 <= n) {
         PackV<In, 8> r;

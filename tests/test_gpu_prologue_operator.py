@@ -405,3 +405,24 @@ def test_one_channel_not_finite(d, lens, dtype, value):
         # (no tolerance, NaN, at the zeros that dividing by an infinite norm leaves: those are exact)
         ref.check(m, x[fin], (y[fin], np.nan_to_num(tol[fin])))
     assert value == value or (np.isnan(want[0][0][at, 1]).all() and np.isnan(wantg['bias_q'][0].reshape(2, d)[1]).all())
+
+
+@pytest.mark.parametrize('grad', ['f32', 'bf16'])
+@pytest.mark.parametrize('gates', ['channel', 'head'])
+def test_gradient_of_large_logits(gates, grad):
+    """The sigmoid's gradient s (1 - s), where s is next to one or to zero, to the precision of its type.
+
+    Tolerance: with e = exp(-|x|), off by 2^-22 + |x| 2^-24 of itself (8 + 2 |x| units of 2^-24 with the rounding of
+    its argument), the gradient is d e / (1 + e)^2: 1 + e one rounding, its reciprocal 2^-23 and squared, two
+    products; 16 units in all. Below the smallest normal float anything may be zero."""
+    p = Batch(19, [64], H=4, dk=16, dv=16, dtype='f32', gates=gates)
+    for x in p.logits:
+        x[:] = np.linspace(-90, 90, x.size, dtype=np.float32).reshape(x.shape)
+    raw, weight, bias, _, cu = p.gpu()
+    grads = [torch.from_numpy(x).to(DEV).unsqueeze(0) for x in p.grads]
+    g = gdn2.prologue_bwd(*raw, weight, bias, *grads, cu, grad_dtype=DT[grad])
+    for m, x, d in zip(('b_logit', 'w_logit'), p.logits, p.grads[3:]):
+        x, d = x.astype(np.float64), d.astype(np.float64)
+        e = np.exp(-np.abs(x))
+        want = d * e / (1 + e) ** 2
+        ref.check(m, back(g[m])[0], (want, ref.rounded(want, np.abs(want) * (16 + 2 * np.abs(x)) * ref.U, grad)))
