@@ -483,11 +483,21 @@ int gdn2_decode_step_prologue(const void *q_raw, const void *k_raw, const void *
 static bool dtype_ok(int t) { return t == GDN2_F32 || t == GDN2_BF16; }
 
 // Whether an output is an input's own memory (partial overlaps are the caller's).
-static bool same_memory(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins)
+using Ptrs = std::initializer_list<const void *>;
+static bool same_memory(Ptrs outs, Ptrs ins)
 {
     for (const void *o : outs)
         for (const void *i : ins)
             if (o && o == i) return true;
+    return false;
+}
+
+// Whether two outputs are one.
+static bool twice(Ptrs outs)
+{
+    for (auto o = outs.begin(); o != outs.end(); ++o)
+        for (auto p = outs.begin(); p != o; ++p)
+            if (*o && *o == *p) return true;
     return false;
 }
 
@@ -521,7 +531,9 @@ int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float 
     const void *ptrs[] = {q, k, v, log_alpha, b, w, state, slot_in, slot_out, commit, o, cu_seqlens};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
-    if (same_memory({o}, {q, k, v, log_alpha, b, w, state})) return GDN2_ERR_INVALID;
+    if (!have_tokens) o = nullptr;   // (nothing is written there)
+    if (o == state || same_memory({o, state}, {q, k, v, log_alpha, b, w, slot_in, slot_out, commit, cu_seqlens}))
+        return GDN2_ERR_INVALID;
     gdn2::RecurrentArgs a;
     a.q = q; a.k = k; a.v = v; a.b = b; a.w = w;
     a.log_alpha = log_alpha;
@@ -594,7 +606,18 @@ int gdn2_prologue_fwd(const void *q_raw, const void *k_raw, const void *v_raw, c
     const void *ptrs[] = {q, k, v, b, w, slot_out, commit};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
-    if (same_memory({q, k, v}, {q_raw, k_raw, v_raw, b_logit, w_logit}) || same_memory({b, w}, {q_raw, k_raw, v_raw}))
+    if ((long long)B * T == 0) q = k = v = b = w = nullptr;   // (nothing is written there)
+    // gates may take their own logits' place, histories their own pool's
+    const Ptrs outs = {q, k, v, b, w, a.hist_out[0], a.hist_out[1], a.hist_out[2]};
+    if (twice(outs) ||
+        same_memory(outs, {q_raw, k_raw, v_raw, a.weight[0], a.weight[1], a.weight[2], a.bias[0], a.bias[1], a.bias[2],
+                           slot_in, slot_out, commit, cu_seqlens}) ||
+        same_memory({q, k, v, b, w}, {a.hist_in[0], a.hist_in[1], a.hist_in[2]}) ||
+        same_memory({a.hist_out[0], a.hist_out[1], a.hist_out[2]}, {b_logit, w_logit}) ||
+        same_memory({q, k, v}, {b_logit, w_logit}) || same_memory({b}, {w_logit}) || same_memory({w}, {b_logit}) ||
+        same_memory({a.hist_out[0]}, {a.hist_in[1], a.hist_in[2]}) ||
+        same_memory({a.hist_out[1]}, {a.hist_in[0], a.hist_in[2]}) ||
+        same_memory({a.hist_out[2]}, {a.hist_in[0], a.hist_in[1]}))
         return GDN2_ERR_INVALID;
     a.y[0] = q; a.y[1] = k; a.y[2] = v;
     a.gate[0] = b; a.gate[1] = w;
@@ -633,8 +656,13 @@ int gdn2_prologue_bwd(const void *q_raw, const void *k_raw, const void *v_raw, c
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
     if (!workspace || workspace_bytes < gdn2_prologue_bwd_workspace_bytes(B, T, N, H, HK, dk, dv, cu_seqlens != nullptr))
         return GDN2_ERR_WORKSPACE;
-    if (same_memory({dq_raw, dk_raw, dv_raw, db_logit, dw_logit},
-                    {q_raw, k_raw, v_raw, b_logit, w_logit, dq, dk_, dv_, db, dw}))
+    if ((long long)B * T == 0) dq_raw = dk_raw = dv_raw = db_logit = dw_logit = nullptr;   // (nothing is written there)
+    const Ptrs outs = {dq_raw, dk_raw, dv_raw, db_logit, dw_logit, dweight_q, dweight_k, dweight_v,
+                       dbias_q, dbias_k, dbias_v, workspace};
+    if (twice(outs) ||
+        same_memory(outs, {q_raw, k_raw, v_raw, b_logit, w_logit, dq, dk_, dv_, db, dw, a.f.weight[0], a.f.weight[1],
+                           a.f.weight[2], a.f.bias[0], a.f.bias[1], a.f.bias[2], a.f.hist_in[0], a.f.hist_in[1],
+                           a.f.hist_in[2], slot_in, cu_seqlens}))
         return GDN2_ERR_INVALID;
     a.dy[0] = dq; a.dy[1] = dk_; a.dy[2] = dv_;
     a.dgate[0] = db; a.dgate[1] = dw;
@@ -703,7 +731,9 @@ int gdn2_layer_norm_bwd(const void *dy, const void *h, const float *weight, cons
         if (p && !aligned16(p)) return GDN2_ERR_INVALID;
     if (!workspace || workspace_bytes < gdn2_layer_norm_bwd_workspace_bytes(rows, cols)) return GDN2_ERR_WORKSPACE;
     if (in_dtype != out_dtype && same_memory({dh}, {dy})) return GDN2_ERR_INVALID;
-    if (same_memory({dh, dweight, dbias}, {weight}) || same_memory({dweight, dbias}, {dy, h, dsum, dh}))
+    if (rows == 0) dh = nullptr;   // (nothing is written there)
+    if (twice({dh, dweight, dbias, workspace}) || same_memory({dh, dweight, dbias, workspace}, {weight}) ||
+        same_memory({dweight, dbias, workspace}, {dy, h, dsum}))
         return GDN2_ERR_INVALID;
     gdn2::LayerNormBwdArgs a;
     a.dy = dy;

@@ -385,13 +385,14 @@ int gdn2_chunk_bwd_kept(const void *q, const void *k, const void *v, const float
  * slot_out. Several sequences may start from one slot; no slot may be written
  * by two sequences of a call, nor written by one and read by another. Slots
  * that no sequence writes, and rows of o behind the last sequence, are left as
- * they were. o overlaps no input. Unlike elsewhere, log_alpha may be -infinity
+ * they were. o and state overlap neither each other nor an input. Unlike elsewhere, log_alpha may be -infinity
  * (a full forget).
  * A NaN or infinity in a token reaches that token and later ones of its
  * sequence, never an earlier token or a prefix kept without it.
  *
  * dk, dv in {16, 32, 64, 128}. GDN2_ERR_INVALID also for HK not dividing H,
- * slots < 1, slot_in NULL with slots < N, or an output that is an input.
+ * slots < 1, slot_in NULL with slots < N, or an output's pointer that is also
+ * an input's or the other output's (partial overlaps are not checked).
  */
 int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float *log_alpha, const void *b,
                        const void *w, int gates, float *state, const int32_t *slot_in, const int32_t *slot_out,
@@ -418,12 +419,17 @@ int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float 
  *                        slot_in (none: zeros), the last three up to its first
  *                        commit[i] tokens go to slot_out. state_out_* may be
  *                        state_in_* (the pools updated in place).
- *   q, k, v, b, w        shaped like the raw tensors, in_dtype; b and w may be
- *                        their logits, the others must not overlap an input
+ *   q, k, v, b, w        shaped like the raw tensors, in_dtype
+ *
+ * b may be b_logit and w w_logit, each of state_out_* the state_in_* of the same
+ * tensor; otherwise no output may overlap an input, a weight, a history or
+ * another output (GDN2_ERR_INVALID where two pointers are one; partial overlaps
+ * are not checked).
  *
  * Sizes, cu_seqlens and errors as in gdn2_recurrent_fwd (slots counts only
  * where a history is given); rows behind the last sequence are left as they
- * were.
+ * were. The squares of a head's convolved channels are added in fp32: above
+ * about 1e19 their sum is infinite and the unit vector zero.
  */
 int gdn2_prologue_fwd(const void *q_raw, const void *k_raw, const void *v_raw, const void *b_logit,
                       const void *w_logit, int gates, const gdn2_short_conv *conv, const int32_t *slot_in,
@@ -437,7 +443,9 @@ int gdn2_prologue_fwd(const void *q_raw, const void *k_raw, const void *v_raw, c
  * logits (grad_dtype: GDN2_F32 or GDN2_BF16) and of taps and biases (float,
  * [heads*d, 4] and [heads*d]; the three dbias pointers may each be NULL).
  * conv: weights, biases and state_in as in the forward (state_out is not
- * used); histories are taken as constants. No output may overlap an input.
+ * used); histories are taken as constants. No output, nor the workspace, may
+ * overlap an input or another output (GDN2_ERR_INVALID where two pointers are
+ * one).
  * workspace: gdn2_prologue_bwd_workspace_bytes(...) of device memory. The
  * taps' sums run in a fixed order: the same inputs give the same bits. Rows of
  * the raw gradients behind the last sequence are left as they were.
@@ -472,7 +480,9 @@ int gdn2_prologue_bwd(const void *q_raw, const void *k_raw, const void *v_raw, c
  * gradient of x and of residual alike), plus dsum (in_dtype) where not NULL:
  * what else depends on h. dweight, dbias [cols] float are summed over the rows
  * in a fixed order; dbias may be NULL. dh may be dy, h or dsum itself (same
- * type). workspace: gdn2_layer_norm_bwd_workspace_bytes(...) of device memory.
+ * type); otherwise no output, nor the workspace, may overlap an input or another
+ * output (GDN2_ERR_INVALID where two pointers are one).
+ * workspace: gdn2_layer_norm_bwd_workspace_bytes(...) of device memory.
  *
  * rows >= 0, 1 <= cols <= GDN2_LAYER_NORM_MAX_COLS, eps > 0, each finite.
  * Pointers are 16-byte aligned; cols may be any number (a multiple of 8 is

@@ -426,3 +426,13 @@ def test_gradient_of_large_logits(gates, grad):
         e = np.exp(-np.abs(x))
         want = d * e / (1 + e) ** 2
         ref.check(m, back(g[m])[0], (want, ref.rounded(want, np.abs(want) * (16 + 2 * np.abs(x)) * ref.U, grad)))
+
+
+def test_gates_over_their_logits():
+    """b and w written over their own logits, the histories over their own pools."""
+    p = Batch(21, SHORT, H=2, dk=32, dv=64, slots=9)
+    raw, weight, bias, hist, cu = p.gpu()
+    want = gdn2.prologue_fwd(*raw, weight, bias, cu, conv_state=hist)
+    q, k, v = (torch.empty_like(x) for x in raw[:3])
+    got = gdn2.prologue_fwd(*raw, weight, bias, cu, conv_state=hist, conv_state_out=hist, out=(q, k, v, raw[3], raw[4]))
+    assert got[3] is raw[3] and all(torch.equal(x, y) for x, y in zip(got, want))

@@ -170,6 +170,59 @@ def test_prologue_bwd_rejects_an_output_that_is_an_input(out, name):
     assert prologue_bwd(**at) == INVALID
 
 
+def _apart(*names):
+    return {n: (i + 2) * P for i, n in enumerate(names)}
+
+
+@pytest.mark.parametrize('name', ['q', 'k', 'v', 'la', 'b', 'w', 'slot_in', 'slot_out', 'commit', 'cu', 'o'])
+def test_recurrent_rejects_states_that_are_another_argument(name):
+    at = _apart('q', 'k', 'v', 'la', 'b', 'w', 'slot_in', 'slot_out', 'commit', 'cu', 'o')
+    assert recurrent(**at, state=at[name], B=1, T=6) == INVALID
+    if name != 'o':
+        assert recurrent(**{**at, 'o': at[name]}, state=P, B=1, T=6) == INVALID
+
+
+CONV = ('weight_q', 'weight_k', 'weight_v', 'bias_q', 'bias_k', 'bias_v', 'state_in_q', 'state_in_k', 'state_in_v',
+        'state_out_q', 'state_out_k', 'state_out_v')
+FWD = ('q', 'k', 'v', 'xb', 'xw', 'slot_in', 'slot_out', 'commit', 'yq', 'yk', 'yv', 'yb', 'yw')
+BWD = ('q', 'k', 'v', 'xb', 'xw', 'slot_in', 'dq', 'dk_', 'dv_', 'db', 'dw', 'gq', 'gk', 'gv', 'gb', 'gw', 'wq', 'wk',
+       'wv', 'bq', 'bk', 'bv', 'ws')
+
+
+def _call(fn, names, at):
+    return fn(**{n: at[n] for n in names}, conv=conv(**{n: at[n] for n in CONV}), slots=2)
+
+
+@pytest.mark.parametrize('out', ['yq', 'yk', 'yv', 'yb', 'yw', 'state_out_q', 'state_out_k', 'state_out_v'])
+def test_prologue_fwd_rejects_an_output_that_is_another_argument(out):
+    """Every other argument but a gate's own logits and a history's own pool."""
+    own = {'yb': 'xb', 'yw': 'xw'}.get(out, out.replace('out', 'in'))
+    for name in (*FWD, *CONV):
+        if name not in (out, own):
+            at = _apart(*FWD, *CONV)
+            at[out] = at[name]
+            assert _call(prologue_fwd, FWD, at) == INVALID, name
+
+
+@pytest.mark.parametrize('out', ['gq', 'gk', 'gv', 'gb', 'gw', 'wq', 'wk', 'wv', 'bq', 'bk', 'bv', 'ws'])
+def test_prologue_bwd_rejects_an_output_that_is_another_argument(out):
+    for name in (*BWD, *CONV[:9]):
+        if name != out:
+            at = _apart(*BWD, *CONV)
+            at[out] = at[name]
+            assert _call(prologue_bwd, BWD, at) == INVALID, name
+
+
+def test_layer_norm_bwd_rejects_an_output_that_is_another_argument():
+    names = ('dy', 'h', 'w', 'ds', 'dh', 'dw', 'db', 'ws')
+    for out in ('dh', 'dw', 'db', 'ws'):
+        for name in names:
+            if name != out and not (out == 'dh' and name in ('dy', 'h', 'ds')):
+                at = _apart(*names)
+                at[out] = at[name]
+                assert layer_norm_bwd(**at, odt=BF16) == INVALID, (out, name)
+
+
 # ---- the Python binding: wrong shapes, types and devices raise before the library is called
 
 def _mix(B=1, T=4, H=2, HK=2, dk=32, dv=32, dt=torch.bfloat16):
