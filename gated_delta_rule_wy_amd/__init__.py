@@ -668,6 +668,8 @@ def _conv_pools(conv_weight, conv_bias, conv_state, conv_state_out, heads, dims,
     addr = [None] * 12   # the struct's fields in order
     slots, f32 = 0, torch.float32
     for z, (t, h, d) in enumerate(zip(conv_weight, heads, dims)):
+        if t is None:
+            raise ValueError('conv_weight: none of the triple may be None')
         _need(t, 'conv_weight', (h * d, 4), f32, dev)
         addr[z] = t.data_ptr()
     if conv_bias is not None:
@@ -686,7 +688,9 @@ def _conv_pools(conv_weight, conv_bias, conv_state, conv_state_out, heads, dims,
             addr[9:] = addr[6:9]
             continue
         for z, (t, h, d) in enumerate(zip(trip, heads, dims)):
-            slots = slots or t.shape[0]
+            if t is None:
+                raise ValueError('conv_state: all three of the triple or none (None instead of it)')
+            slots = slots or (t.shape[0] if t.dim() else 0)
             _need(t, 'conv_state', (slots, h, 3, d), dt, dev)
             addr[at + z] = t.data_ptr()
     return ShortConv(*addr), slots

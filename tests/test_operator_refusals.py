@@ -317,6 +317,27 @@ def test_prologue_binding_refuses(change):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize('z', [0, 1, 2])
+@pytest.mark.parametrize('name', ['conv_weight', 'conv_state', 'conv_state_out'])
+@pytest.mark.parametrize('value', [None, 0])
+def test_prologue_binding_refuses_a_triple_with_a_gap(name, z, value):
+    """None in a triple, and a tensor without axes."""
+    dev = torch.device('cuda:0')
+    q, k, v, _, b, w = (t.to(dev) for t in _mix())
+    pool = [torch.zeros(2, 2, 3, 32, dtype=torch.bfloat16, device=dev) for _ in range(3)]
+    kw = dict(conv_weight=[torch.zeros(64, 4, device=dev) for _ in range(3)], conv_state=pool, conv_state_out=list(pool))
+    kw[name] = list(kw[name])
+    kw[name][z] = None if value is None else torch.zeros((), dtype=kw[name][z].dtype, device=dev)
+    with pytest.raises(ValueError, match='conv_weight' if name == 'conv_weight' else 'conv_state'):
+        gdn2.prologue_fwd(q, k, v, b, w, **kw)
+    if name != 'conv_state_out':
+        grads = [torch.zeros(x.shape, device=dev) for x in (q, k, v, b, w)]
+        del kw['conv_state_out']
+        with pytest.raises(ValueError, match=name):
+            gdn2.prologue_bwd(q, k, v, b, w, kw.pop('conv_weight'), None, *grads, **kw)
+
+
+@pytest.mark.gpu
 def test_layer_norm_binding_refuses():
     dev = torch.device('cuda:0')
     x, w = torch.zeros(4, 16, device=dev), torch.ones(16, device=dev)
