@@ -501,6 +501,12 @@ static bool twice(Ptrs outs)
     return false;
 }
 
+// Sizes whose launch would have too many threads are found where it is laid out.
+static int launch_status(hipError_t err)
+{
+    return err == hipSuccess ? GDN2_OK : err == hipErrorInvalidConfiguration ? GDN2_ERR_UNSUPPORTED : GDN2_ERR_HIP;
+}
+
 // Sizes shared by the recurrence on slots and the prologue.
 static int serve_check(int B, int T, int N, int H, int HK, int dk, int dv, int in_dtype, int varlen)
 {
@@ -525,7 +531,8 @@ int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float 
     const int st = serve_check(B, T, N, H, HK, dk, dv, in_dtype, cu_seqlens != nullptr);
     if (st != GDN2_OK) return st;
     if (!dtype_ok(out_dtype) || slots < 1 || (!slot_in && slots < N)) return GDN2_ERR_INVALID;
-    if ((long long)N * H * (dv / 16) > 0x7fffffffLL) return GDN2_ERR_UNSUPPORTED;   // grid
+    // (a wave has 16 columns of a chain, and a launch fewer than 2^32 threads)
+    if ((long long)N * H * (dv / 16) * 64 > 0xffffffffLL) return GDN2_ERR_UNSUPPORTED;
     const bool have_tokens = (long long)B * T > 0;
     if (!state || (have_tokens && (!q || !k || !v || !log_alpha || !b || !w || !o))) return GDN2_ERR_INVALID;
     const void *ptrs[] = {q, k, v, log_alpha, b, w, state, slot_in, slot_out, commit, o, cu_seqlens};
@@ -624,7 +631,7 @@ int gdn2_prologue_fwd(const void *q_raw, const void *k_raw, const void *v_raw, c
     a.slot_out = slot_out;
     a.commit = commit;
     prof_call();
-    return gdn2::launch_prologue_fwd(a, g_stream) == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+    return launch_status(gdn2::launch_prologue_fwd(a, g_stream));
 }
 
 size_t gdn2_prologue_bwd_workspace_bytes(int B, int T, int N, int H, int HK, int dk, int dv, int varlen)
@@ -673,7 +680,7 @@ int gdn2_prologue_bwd(const void *q_raw, const void *k_raw, const void *v_raw, c
     a.dbias[0] = dbias_q; a.dbias[1] = dbias_k; a.dbias[2] = dbias_v;
     a.workspace = workspace;
     prof_call();
-    return gdn2::launch_prologue_bwd(a, g_stream) == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+    return launch_status(gdn2::launch_prologue_bwd(a, g_stream));
 }
 
 static int layer_norm_check(int64_t rows, int cols, float eps, int in_dtype, int out_dtype)

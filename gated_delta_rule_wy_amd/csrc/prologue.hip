@@ -606,10 +606,15 @@ __global__ __launch_bounds__(kNT) void prologue_bwd_kernel(ProBwdParams p)
 
 static int64_t tokens_of(const PrologueArgs &a) { return a.cu_seqlens ? (int64_t)a.T : (int64_t)a.N * a.T; }
 
-static ProParams pro_params(const PrologueArgs &a, int V, int64_t tiles, int tile, int *blocks)
+// A launch takes fewer than 2^32 threads.
+constexpr int64_t kMostBlocks = 0xFFFFFFFFLL / kNT;
+
+// blocks: how many workgroups these take (the parameters hold their numbers
+// where it is at most kMostBlocks)
+static ProParams pro_params(const PrologueArgs &a, int V, int64_t tiles, int tile, int64_t *blocks)
 {
     ProParams p = {};
-    int at = 0;
+    int64_t at = 0;
     for (int z = 0; z < 3; ++z) {
         ProTensor &t = p.t[z];
         t.x = a.x[z];
@@ -624,18 +629,20 @@ static ProParams pro_params(const PrologueArgs &a, int V, int64_t tiles, int til
         const int nvec = t.heads * t.d / V;
         t.per = nvec >= kNT ? (nvec + kNT - 1) / kNT : 0;
         t.rows = nvec >= kNT ? 0 : kNT / nvec;
-        t.block0 = at;
-        t.blocks = (int)(t.per ? tiles * t.per : (tiles + t.rows - 1) / t.rows);
-        at += t.blocks;
+        const int64_t n = t.per ? tiles * t.per : (tiles + t.rows - 1) / t.rows;
+        t.block0 = (int)at;
+        t.blocks = (int)n;
+        at += n;
     }
     for (int z = 0; z < 2; ++z) {
         ProGate &g = p.g[z];
         g.x = a.logit[z];
         g.y = a.gate[z];
         g.n = a.nlogit[z];
-        g.block0 = at;
-        g.blocks = (int)((tokens_of(a) * g.n + 8 * kNT - 1) / (8 * kNT));
-        at += g.blocks;
+        const int64_t n = (tokens_of(a) * g.n + 8 * kNT - 1) / (8 * kNT);
+        g.block0 = (int)at;
+        g.blocks = (int)n;
+        at += n;
     }
     p.sq = {a.cu_seqlens, a.T, a.N};
     p.slot_in = a.slot_in;
@@ -675,14 +682,15 @@ template <typename In> static hipError_t prologue_fwd_t(const PrologueArgs &a, h
     // and 19 with a tile each)
     const int tile = tile_of(tokens, channels, kFwdV, std::min<long long>(4, tokens / a.N),
                              std::min<long long>(64, 2 * tokens / a.N));
-    int blocks = 0;
+    int64_t blocks = 0;
     ProParams p = pro_params(a, kFwdV, own ? a.N : (tokens + tile - 1) / tile, tile, &blocks);
-    p.empty0 = blocks;
+    p.empty0 = (int)blocks;
     if (!own && hist && a.cu_seqlens) blocks += a.N;
     if (blocks == 0 || (tokens == 0 && !hist)) return hipSuccess;
+    if (blocks > kMostBlocks) return hipErrorInvalidConfiguration;
     prof_before("gdn2_prologue_fwd", st);
-    if (own) hipLaunchKernelGGL((prologue_fwd_kernel<In, true>), dim3(blocks), dim3(kNT), 0, st, p);
-    else hipLaunchKernelGGL((prologue_fwd_kernel<In, false>), dim3(blocks), dim3(kNT), 0, st, p);
+    if (own) hipLaunchKernelGGL((prologue_fwd_kernel<In, true>), dim3((unsigned)blocks), dim3(kNT), 0, st, p);
+    else hipLaunchKernelGGL((prologue_fwd_kernel<In, false>), dim3((unsigned)blocks), dim3(kNT), 0, st, p);
     prof_after(st);
     return hipGetLastError();
 }
@@ -705,9 +713,10 @@ template <typename In, typename Out> static hipError_t prologue_bwd_t(const Prol
     for (int z = 0; z < 3; ++z) channels += a.f.heads[z] * a.f.d[z];
     const int tile = prologue_bwd_tile(tokens, channels);
     const int64_t tiles = (tokens + tile - 1) / tile;
-    int blocks = 0;
+    int64_t blocks = 0;
     ProBwdParams p = {};
     p.f = pro_params(a.f, kBwdV, tiles, tile, &blocks);
+    if (blocks > kMostBlocks) return hipErrorInvalidConfiguration;
     float *part = (float *)a.workspace;
     ColumnSums cs = {};
     for (int z = 0; z < 3; ++z) {
@@ -728,7 +737,7 @@ template <typename In, typename Out> static hipError_t prologue_bwd_t(const Prol
     }
     if (blocks > 0) {
         prof_before("gdn2_prologue_bwd", st);
-        hipLaunchKernelGGL((prologue_bwd_kernel<In, Out>), dim3(blocks), dim3(kNT), 0, st, p);
+        hipLaunchKernelGGL((prologue_bwd_kernel<In, Out>), dim3((unsigned)blocks), dim3(kNT), 0, st, p);
         prof_after(st);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;

@@ -392,7 +392,8 @@ int gdn2_chunk_bwd_kept(const void *q, const void *k, const void *v, const float
  *
  * dk, dv in {16, 32, 64, 128}. GDN2_ERR_INVALID also for HK not dividing H,
  * slots < 1, slot_in NULL with slots < N, or an output's pointer that is also
- * an input's or the other output's (partial overlaps are not checked).
+ * an input's or the other output's (partial overlaps are not checked), and
+ * GDN2_ERR_UNSUPPORTED for N * H * dv / 16 >= 2^26 (one launch).
  */
 int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float *log_alpha, const void *b,
                        const void *w, int gates, float *state, const int32_t *slot_in, const int32_t *slot_out,
@@ -429,7 +430,8 @@ int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float 
  * Sizes, cu_seqlens and errors as in gdn2_recurrent_fwd (slots counts only
  * where a history is given); rows behind the last sequence are left as they
  * were. The squares of a head's convolved channels are added in fp32: above
- * about 1e19 their sum is infinite and the unit vector zero.
+ * about 1e19 their sum is infinite and the unit vector zero. Sizes that would
+ * take 2^32 threads or more in one launch give GDN2_ERR_UNSUPPORTED.
  */
 int gdn2_prologue_fwd(const void *q_raw, const void *k_raw, const void *v_raw, const void *b_logit,
                       const void *w_logit, int gates, const gdn2_short_conv *conv, const int32_t *slot_in,

@@ -170,6 +170,24 @@ def test_prologue_bwd_rejects_an_output_that_is_an_input(out, name):
     assert prologue_bwd(**at) == INVALID
 
 
+def test_rejects_more_threads_than_a_launch_takes():
+    """2^32 threads or more, of sizes that every other check lets pass."""
+    ins = {n: (i + 2) * P for i, n in enumerate(('q', 'k', 'v', 'la', 'b', 'w', 'state', 'o'))}
+    many = dict(B=1 << 20, N=1 << 20, T=1, H=64, HK=1, slots=1 << 20, dk=128, dv=128)
+    assert recurrent(**ins, **many) == UNSUPPORTED
+    assert recurrent(**ins, **{**many, 'H': 128, 'dk': 64, 'dv': 64}) == UNSUPPORTED
+    at = _apart('q', 'k', 'v', 'xb', 'xw', 'yq', 'yk', 'yv', 'yb', 'yw')
+    many = dict(B=1 << 24, N=1 << 24, T=1, H=15, HK=1, dk=128, dv=128)
+    assert prologue_fwd(**at, **many) == UNSUPPORTED
+    assert prologue_fwd(**at, **many, gates=3) == UNSUPPORTED
+    pools = conv(**{n: (i + 20) * P for i, n in enumerate(('state_out_q', 'state_out_k', 'state_out_v'))})
+    assert prologue_fwd(**at, conv=pools, slots=4, slot_in=50 * P, cu=51 * P, B=1, N=(1 << 31) - 1, T=17, H=1, HK=1,
+                        dk=16, dv=16) == UNSUPPORTED
+    at = {n: (i + 2) * P for i, n in enumerate(('q', 'k', 'v', 'xb', 'xw', 'dq', 'dk_', 'dv_', 'db', 'dw', 'gq', 'gk', 'gv',
+                                                'gb', 'gw', 'wq', 'wk', 'wv', 'ws'))}
+    assert prologue_bwd(**at, **many, wsb=1 << 40) == UNSUPPORTED
+
+
 def _apart(*names):
     return {n: (i + 2) * P for i, n in enumerate(names)}
 
