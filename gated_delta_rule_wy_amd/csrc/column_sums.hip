@@ -6,7 +6,7 @@
 // wave's rows come in a few rounds of eight loads (128 rows of 30720 sums 6 us,
 // 512 of 4096 5 us, most of it the launch's own).
 #include "gdn2_device.hpp"
-#include "gdn2_launch.hpp"
+#include "operators_launch.hpp"
 
 #include <algorithm>
 

@@ -24,7 +24,7 @@
 // Each workgroup adds its rows' terms of dweight and dbias in registers, in
 // row order, and writes one partial row; a second kernel adds the partial
 // rows in a fixed order (no atomics: the same inputs give the same bits).
-#include "gdn2_launch.hpp"
+#include "operators_launch.hpp"
 #include "rows.hpp"
 
 #include <algorithm>

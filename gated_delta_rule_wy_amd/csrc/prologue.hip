@@ -18,7 +18,7 @@
 // (5.6 TB/s) since the histories no longer take a launch of their own; backward
 // over 8 of up to 4096: 368 us with two (5.4 TB/s), 379 with four. All sums are
 // fp32; outputs are rounded once.
-#include "gdn2_launch.hpp"
+#include "operators_launch.hpp"
 #include "rows.hpp"
 
 #include <algorithm>

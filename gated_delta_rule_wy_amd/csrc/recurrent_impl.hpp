@@ -44,7 +44,7 @@
 // cores' rate.
 #pragma once
 
-#include "gdn2_launch.hpp"
+#include "operators_launch.hpp"
 #include "rows.hpp"
 
 #include <type_traits>
