@@ -25,6 +25,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -41,16 +42,31 @@ def log(*a):
     print(*a, file=sys.stderr, flush=True)
 
 
+CSRC = os.path.join(ROOT, 'gated_delta_rule_wy_amd', 'csrc')
+
+
+def timed_sources() -> list:
+    """Files of csrc/ that the kernels timed here are compiled and dispatched
+    from: the chunk and decode kernels, their entry points (api.hip) and
+    whatever those include there. The operators around the mixer are not among
+    them."""
+    todo = [f for f in os.listdir(CSRC) if f == 'api.hip' or f.startswith(('chunk', 'decode'))]
+    seen = set()
+    while todo:
+        f = todo.pop()
+        if f not in seen:
+            seen.add(f)
+            with open(os.path.join(CSRC, f)) as fh:
+                names = re.findall(r'^\s*#\s*include\s*"([^"]+)"', fh.read(), re.M)
+            todo += [n for n in names if os.path.exists(os.path.join(CSRC, n)) and '/' not in n]
+    return sorted(seen)
+
+
 def src_hash() -> str:
-    """Hash of the sources of the kernels timed here (the counter summaries
-    hold the one they were taken on); the operators around the mixer and the
-    host side are not among them."""
+    """Hash of those sources (the counter summaries hold the one they were taken on)."""
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, 'gated_delta_rule_wy_amd', 'csrc')
-    for f in sorted(os.listdir(csrc)):
-        if not f.startswith(('chunk', 'decode', 'gdn2_device')):
-            continue
-        with open(os.path.join(csrc, f), 'rb') as fh:
+    for f in timed_sources():
+        with open(os.path.join(CSRC, f), 'rb') as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]
 
