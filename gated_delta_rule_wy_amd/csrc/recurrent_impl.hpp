@@ -39,9 +39,12 @@
 // 90 us (5.4 TB/s). With more tokens a sequence the blocks come one after the
 // other: about 2.6 us a block of one chain alone, some 6500 cycles, of which
 // a quarter prepares the rows, an eighth forms X in one wave, and the matrix
-// products need 1900; 256 x 16 chains of 64 tokens 407 us; 48 sequences x 16
+// products need 1900; 256 x 16 chains of 64 tokens 418 us; 48 sequences x 16
 // heads of up to 64 fp32 tokens (128 x 64) 42 us, a third of them at the matrix
 // cores' rate.
+// A block that is cut leaves no longer blocks to the rest of its sequence: 48 x
+// 16 chains of 64 fp32 tokens (128 x 64) 55 us, 92 with four channels at e^-8 a
+// token, 317 with one channel forgotten at the fifth token.
 #pragma once
 
 #include "operators_launch.hpp"
