@@ -717,7 +717,7 @@ def prologue_fwd(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor, 
     conv_state_out: (q, k, v) pools of histories, [slots, HK, 3, dk] twice and
     [slots, H, 3, dv], or None for zeros / not written; conv_state_out may be
     conv_state itself. slot_in, slot_out, commit as in ``recurrent_fwd``. out:
-    five tensors to write, or None. Returns (q, k, v, b, w) in the input dtype."""
+    five tensors to write (b and w may be their own logits), or None. Returns (q, k, v, b, w) in the input dtype."""
     dev, dt, gates, B, T, N, H, HK, dk, dv = _prologue_sizes(q_raw, k_raw, v_raw, b_logit, w_logit, cu_seqlens)
     sc, slots = _conv_pools(conv_weight, conv_bias, conv_state, conv_state_out, (HK, HK, H), (dk, dk, dv), dt, dev)
     _index(slot_in, 'slot_in', N, dev)

@@ -385,8 +385,8 @@ int gdn2_chunk_bwd_kept(const void *q, const void *k, const void *v, const float
  * slot_out. Several sequences may start from one slot; no slot may be written
  * by two sequences of a call, nor written by one and read by another. Slots
  * that no sequence writes, and rows of o behind the last sequence, are left as
- * they were. o and state overlap neither each other nor an input. Unlike elsewhere, log_alpha may be -infinity
- * (a full forget).
+ * they were. o and state overlap neither each other nor an input. Unlike
+ * elsewhere, log_alpha may be -infinity (a full forget).
  * A NaN or infinity in a token reaches that token and later ones of its
  * sequence, never an earlier token or a prefix kept without it.
  *
