@@ -14,7 +14,10 @@ sequence and head, state S in R^{dk x dv}:
 Around it, for a whole layer: ``prologue_fwd`` / ``prologue_bwd`` (short
 convolution, unit norm, sigmoid), ``recurrent_fwd`` (the recurrence over a few
 tokens a sequence, its states in a pool) and ``layer_norm_fwd`` /
-``layer_norm_bwd``.
+``layer_norm_bwd``; the layer's dense half: ``linear_fwd`` / ``linear_bwd``
+(projections with bias, activation and residual, in bf16, fp32 or 8 bits),
+``rms_norm_fwd`` / ``rms_norm_bwd`` before them (its output in 8 bits with
+scales, if wanted), and ``grad_norm`` / ``clip_grads`` over a model's gradients.
 """
 from __future__ import annotations
 
@@ -28,7 +31,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, 'libgdn2.so')
 
 GDN2_OK, GDN2_ERR_INVALID, GDN2_ERR_UNSUPPORTED, GDN2_ERR_WORKSPACE, GDN2_ERR_HIP = range(5)
-GDN2_F32, GDN2_BF16 = 0, 1
+GDN2_F32, GDN2_BF16, GDN2_E4M3 = 0, 1, 2
+ACTIVATIONS = {None: 0, 'none': 0, 'sigmoid': 1, 'silu': 2, 'gelu_tanh': 3}
 GDN2_GATES_PER_CHANNEL, GDN2_GATE_B_PER_HEAD, GDN2_GATE_W_PER_HEAD, GDN2_GATE_ALPHA_PER_HEAD = 0, 1, 2, 4
 CHUNK = 64
 
@@ -40,6 +44,9 @@ EXPORTS = ('gdn2_set_stream', 'gdn2_get_stream', 'gdn2_status_string',
            'gdn2_chunk_bwd_workspace_bytes', 'gdn2_chunk_bwd', 'gdn2_chunk_fwd_keep', 'gdn2_chunk_bwd_kept',
            'gdn2_recurrent_fwd', 'gdn2_prologue_fwd', 'gdn2_prologue_bwd_workspace_bytes', 'gdn2_prologue_bwd',
            'gdn2_layer_norm_fwd', 'gdn2_layer_norm_bwd_workspace_bytes', 'gdn2_layer_norm_bwd',
+           'gdn2_linear_fwd', 'gdn2_linear_bwd_workspace_bytes', 'gdn2_linear_bwd',
+           'gdn2_rms_norm_fwd', 'gdn2_rms_norm_bwd_workspace_bytes', 'gdn2_rms_norm_bwd',
+           'gdn2_clip_grads_workspace_bytes', 'gdn2_grad_norm', 'gdn2_clip_grads',
            'gdn2_profile_begin', 'gdn2_profile_end', 'gdn2_profile_kernel')
 
 
@@ -111,6 +118,24 @@ def _load() -> ctypes.CDLL:
     lib.gdn2_layer_norm_bwd_workspace_bytes.restype = sz
     lib.gdn2_layer_norm_bwd.argtypes = [vp] * 7 + [i64, i, f, i, i, vp, sz]
     lib.gdn2_layer_norm_bwd.restype = i
+    lib.gdn2_linear_fwd.argtypes = [vp] * 8 + [i64] + [i] * 5
+    lib.gdn2_linear_fwd.restype = i
+    lib.gdn2_linear_bwd_workspace_bytes.argtypes = [i64] + [i] * 8
+    lib.gdn2_linear_bwd_workspace_bytes.restype = sz
+    lib.gdn2_linear_bwd.argtypes = [vp] * 7 + [i64] + [i] * 5 + [vp, sz]
+    lib.gdn2_linear_bwd.restype = i
+    lib.gdn2_rms_norm_fwd.argtypes = [vp] * 6 + [i64, i, f, i, i]
+    lib.gdn2_rms_norm_fwd.restype = i
+    lib.gdn2_rms_norm_bwd_workspace_bytes.argtypes = [i64, i]
+    lib.gdn2_rms_norm_bwd_workspace_bytes.restype = sz
+    lib.gdn2_rms_norm_bwd.argtypes = [vp] * 6 + [i64, i, f, i, i, vp, sz]
+    lib.gdn2_rms_norm_bwd.restype = i
+    lib.gdn2_clip_grads_workspace_bytes.argtypes = []
+    lib.gdn2_clip_grads_workspace_bytes.restype = sz
+    lib.gdn2_grad_norm.argtypes = [vp, vp, vp, i, vp, vp, sz]
+    lib.gdn2_grad_norm.restype = i
+    lib.gdn2_clip_grads.argtypes = [vp] * 5 + [i, f, vp, i, vp, sz]
+    lib.gdn2_clip_grads.restype = i
     lib.gdn2_profile_begin.argtypes = [i]
     lib.gdn2_profile_begin.restype = i
     lib.gdn2_profile_end.argtypes = []
@@ -861,3 +886,266 @@ def layer_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, *, d
           _addr(dsum), out.data_ptr(), g['weight'].data_ptr(), g['bias'].data_ptr(), rows, cols, eps, _CODES[dt],
           _CODES[dy.dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return g
+
+
+# ---- the layer's dense half: projections, the norm before them, the clipping of their gradients
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _act_code(activation) -> int:
+    code = ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f'unsupported activation {activation!r} (one of {[a for a in ACTIVATIONS if a]})')
+    return code
+
+
+def _linear_sizes(x, weight, name='x'):
+    """Device, dtype, leading shape, rows, in_features and out_features of a linear layer, checked."""
+    dev, dt = _gpu(x, name), x.dtype
+    if x.dim() < 1 or weight.dim() != 2 or weight.shape[0] < 1 or weight.shape[1] < 1:
+        raise ValueError(f'{name} must be [..., in_features] and weight [out_features, in_features], of one at least')
+    N, K = weight.shape
+    lead = x.shape[:-1]
+    if x.shape[-1] != K:
+        raise ValueError(f'{name}: expected {K} in_features, got {x.shape[-1]}')
+    if not x.is_contiguous():
+        raise ValueError(f'{name}: must be contiguous')
+    _need(weight, 'weight', (N, K), dt, dev)
+    return dev, dt, lead, x.numel() // K, K, N
+
+
+def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, *, activation: Optional[str] = None,
+               x_scale: Optional[torch.Tensor] = None, weight_scale: Optional[torch.Tensor] = None,
+               out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, output_preact: bool = False,
+               preact_out: Optional[torch.Tensor] = None):
+    """act(x weight^T + bias) + residual (gdn2_linear_fwd). x: [..., in_features],
+    weight: [out_features, in_features], one dtype: bf16, fp32, or float8_e4m3fn
+    with fp32 x_scale ([...], x's leading shape) and weight_scale [out_features],
+    which multiply the product. bias: [out_features] fp32. residual:
+    [..., out_features] in the output's dtype. activation: None, 'sigmoid',
+    'silu' or 'gelu_tanh'. Returns (y in ``out_dtype`` (None: x's; bf16 for 8 bits),
+    z or None): z, the activation's argument in x's dtype, is what ``linear_bwd``
+    takes, with ``output_preact`` or into ``preact_out``. ``out`` may be the residual."""
+    dev, dt, lead, M, K, N = _linear_sizes(x, weight)
+    act = _act_code(activation)
+    e4m3 = dt is _E4M3
+    if not e4m3:
+        _dtype_code(x)
+        if x_scale is not None or weight_scale is not None:
+            raise ValueError('x_scale and weight_scale: only with float8_e4m3fn operands')
+    else:
+        if x_scale is None or weight_scale is None:
+            raise ValueError('float8_e4m3fn operands need x_scale and weight_scale')
+        _need(x_scale, 'x_scale', lead, torch.float32, dev)
+        _need(weight_scale, 'weight_scale', (N,), torch.float32, dev)
+        if output_preact or preact_out is not None:
+            raise ValueError('preact: not with float8_e4m3fn operands')
+    out_dtype = out.dtype if out is not None else (torch.bfloat16 if e4m3 else dt) if out_dtype is None else out_dtype
+    if out_dtype not in _CODES:
+        raise TypeError(f'unsupported output dtype {out_dtype} (bfloat16 or float32)')
+    shape = (*lead, N)
+    if bias is not None:
+        _need(bias, 'bias', (N,), torch.float32, dev)
+    if residual is not None:
+        _need(residual, 'residual', shape, out_dtype, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        _need(out, 'out', shape, out_dtype, dev)
+    if preact_out is not None:
+        _need(preact_out, 'preact_out', shape, dt, dev)
+    elif output_preact:
+        preact_out = torch.empty(shape, dtype=dt, device=dev)
+    _call(_lib.gdn2_linear_fwd, 'gdn2_linear_fwd', dev, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(residual),
+          _addr(x_scale), _addr(weight_scale), out.data_ptr(), _addr(preact_out), M, K, N, act,
+          GDN2_E4M3 if e4m3 else _CODES[dt], _CODES[out_dtype])
+    return out, preact_out
+
+
+def linear_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, preact: Optional[torch.Tensor] = None, *,
+               activation: Optional[str] = None, output_x: bool = True, output_weight: bool = True,
+               output_bias: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradient of ``linear_fwd`` (gdn2_linear_bwd) from dy: [..., out_features]
+    (bf16 or fp32, the forward's output dtype), x, weight and, with an
+    activation, the z that the forward returned. Returns {'x': dL/dx, 'weight':
+    dL/dweight} in x's dtype (bf16 or fp32) and {'bias': fp32}, each if its
+    flag is set. The residual's gradient is dy itself."""
+    dev, dt, lead, M, K, N = _linear_sizes(x, weight)
+    _dtype_code(x)
+    act = _act_code(activation)
+    shape = (*lead, N)
+    if dy.dtype not in _CODES:
+        raise TypeError(f'unsupported gradient dtype {dy.dtype} (bfloat16 or float32)')
+    _need(dy, 'dy', shape, dy.dtype, dev)
+    if act and preact is None:
+        raise ValueError(f'preact: {activation} needs what linear_fwd returned')
+    if preact is not None:
+        _need(preact, 'preact', shape, dt, dev)
+    if not (output_x or output_weight or output_bias):
+        raise ValueError('none of the gradients is wanted')
+    g = {}
+    if output_x:
+        g['x'] = torch.empty_like(x)
+    if output_weight:
+        g['weight'] = torch.empty_like(weight)
+    if output_bias:
+        g['bias'] = torch.empty(N, dtype=torch.float32, device=dev)
+    codes = _CODES[dt], _CODES[dy.dtype]
+    need = _lib.gdn2_linear_bwd_workspace_bytes(M, K, N, act, *codes, output_x, output_weight, output_bias)
+    if need == 0:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, 'gdn2_linear_bwd_workspace_bytes')
+    workspace = _workspace(workspace, need, dev)
+    _call(_lib.gdn2_linear_bwd, 'gdn2_linear_bwd', dev, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _addr(preact),
+          _addr(g.get('x')), _addr(g.get('weight')), _addr(g.get('bias')), M, K, N, act, *codes, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return g
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, dev) -> torch.Tensor:
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f'workspace: must be contiguous on {dev}')
+    return workspace
+
+
+def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
+                 output_sum: bool = False, out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                 scale_out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None):
+    """RMS norm of x + residual over the last axis (gdn2_rms_norm_fwd). x,
+    residual: [..., cols], one dtype (bf16 or fp32); weight: [cols] fp32. Returns
+    (y, h or None, scale or None): y in ``out_dtype`` (None: x's; bf16, fp32 or
+    float8_e4m3fn); h = x + residual, what ``rms_norm_bwd`` takes, with
+    ``output_sum`` or into ``sum_out``; scale: [...] fp32, with float8_e4m3fn
+    alone: y times its row's scale is the norm, and ``linear_fwd`` takes both.
+    ``out`` (same dtype) and ``sum_out`` may be x or residual itself."""
+    dev, dt, shape = _gpu(x, 'x'), x.dtype, x.shape
+    _dtype_code(x)
+    if x.dim() < 1 or shape[-1] < 1:
+        raise ValueError('x must be [..., cols] with cols >= 1')
+    cols = shape[-1]
+    if not x.is_contiguous():
+        raise ValueError('x: must be contiguous')
+    _need(weight, 'weight', (cols,), torch.float32, dev)
+    if residual is not None:
+        _need(residual, 'residual', shape, dt, dev)
+    if sum_out is not None:
+        _need(sum_out, 'sum_out', shape, dt, dev)
+    elif output_sum:
+        sum_out = torch.empty_like(x)
+    out_dtype = out.dtype if out is not None else (dt if out_dtype is None else out_dtype)
+    e4m3 = out_dtype is _E4M3
+    if not e4m3 and out_dtype not in _CODES:
+        raise TypeError(f'unsupported output dtype {out_dtype} (bfloat16, float32 or float8_e4m3fn)')
+    if out is None:
+        out = torch.empty_like(x) if out_dtype is dt else torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        _need(out, 'out', shape, out_dtype, dev)
+    if scale_out is not None:
+        if not e4m3:
+            raise ValueError('scale_out: only with a float8_e4m3fn output')
+        _need(scale_out, 'scale_out', shape[:-1], torch.float32, dev)
+    elif e4m3:
+        scale_out = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    _call(_lib.gdn2_rms_norm_fwd, 'gdn2_rms_norm_fwd', dev, x.data_ptr(), _addr(residual), weight.data_ptr(),
+          out.data_ptr(), _addr(scale_out), _addr(sum_out), x.numel() // cols, cols, eps, _CODES[dt],
+          GDN2_E4M3 if e4m3 else _CODES[out_dtype])
+    return out, sum_out, scale_out
+
+
+def rms_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, *, dsum: Optional[torch.Tensor] = None,
+                 eps: float = 1e-5, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradient of ``rms_norm_fwd`` (gdn2_rms_norm_bwd). h: [..., cols], the sum
+    the forward returned (x where there was no residual); dy: shaped like it,
+    bf16 or fp32; dsum: a further gradient of h, added on. Returns {'x': dL/dh (of
+    x and of residual alike) in h's dtype, 'weight': fp32 [cols]}."""
+    dev, dt, shape = _gpu(h, 'h'), h.dtype, h.shape
+    _dtype_code(h)
+    if h.dim() < 1 or shape[-1] < 1:
+        raise ValueError('h must be [..., cols] with cols >= 1')
+    cols = shape[-1]
+    rows = h.numel() // cols
+    if dy.dtype not in _CODES:
+        raise TypeError(f'unsupported gradient dtype {dy.dtype} (bfloat16 or float32)')
+    if not h.is_contiguous():
+        raise ValueError('h: must be contiguous')
+    _need(dy, 'dy', shape, dy.dtype, dev)
+    _need(weight, 'weight', (cols,), torch.float32, dev)
+    if dsum is not None:
+        _need(dsum, 'dsum', shape, dt, dev)
+    if out is None:
+        out = torch.empty_like(h)
+    else:
+        _need(out, 'out', shape, dt, dev)
+    g = {'x': out, 'weight': torch.empty_like(weight)}
+    need = _lib.gdn2_rms_norm_bwd_workspace_bytes(rows, cols)
+    if need == 0:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, 'gdn2_rms_norm_bwd_workspace_bytes')
+    workspace = _workspace(workspace, need, dev)
+    _call(_lib.gdn2_rms_norm_bwd, 'gdn2_rms_norm_bwd', dev, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _addr(dsum),
+          out.data_ptr(), g['weight'].data_ptr(), rows, cols, eps, _CODES[dt], _CODES[dy.dtype], workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return g
+
+
+def _tensor_list(tensors, name):
+    """Addresses, element counts and dtype codes of tensors on one GPU, as ctypes arrays."""
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError(f'{name}: no tensors')
+    n, dev = len(tensors), _gpu(tensors[0], name)
+    ptrs, sizes, types = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    for i, t in enumerate(tensors):
+        code = _CODES.get(t.dtype)
+        if code is None:
+            raise TypeError(f'{name}[{i}]: unsupported dtype {t.dtype} (bfloat16 or float32)')
+        if t.device != dev:
+            raise ValueError(f'{name}[{i}]: expected device {dev}, got {t.device}')
+        if not t.is_contiguous():
+            raise ValueError(f'{name}[{i}]: must be contiguous')
+        ptrs[i], sizes[i], types[i] = t.data_ptr(), t.numel(), code
+    return tensors, dev, ptrs, sizes, types
+
+
+def grad_norm(grads, *, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The norm over all elements of a list of bf16 and fp32 tensors on one GPU
+    (gdn2_grad_norm), an fp32 tensor without axes."""
+    _, dev, ptrs, sizes, types = _tensor_list(grads, 'grads')
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    workspace = _workspace(workspace, _lib.gdn2_clip_grads_workspace_bytes(), dev)
+    _call(_lib.gdn2_grad_norm, 'gdn2_grad_norm', dev, ptrs, sizes, types, len(sizes), norm.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return norm
+
+
+def clip_grads(grads, max_norm: float, *, out=None, norm: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Scale a list of bf16 and fp32 tensors on one GPU by min(1, max_norm / (norm +
+    1e-6)), in place or into the tensors of ``out`` (same shapes, bf16 or fp32;
+    each may be its gradient itself, none may overlap another)
+    (gdn2_clip_grads). norm: the global norm to go by, an fp32 tensor of one element on the
+    device (a norm over several devices' parts, say), or None for that of
+    ``grads``. Returns the norm."""
+    grads, dev, ptrs, sizes, types = _tensor_list(grads, 'grads')
+    optrs, otypes = ptrs, types
+    if out is not None:
+        out, odev, optrs, osizes, otypes = _tensor_list(out, 'out')
+        if len(out) != len(grads) or odev != dev:
+            raise ValueError(f'out: expected {len(grads)} tensors on {dev}, got {len(out)} on {odev}')
+        for i, (t, o) in enumerate(zip(grads, out)):
+            if t.shape != o.shape:
+                raise ValueError(f'out[{i}]: expected shape {tuple(t.shape)}, got {tuple(o.shape)}')
+    given = norm is not None
+    if given:
+        if norm.numel() != 1 or norm.dtype != torch.float32 or norm.device != dev:
+            raise ValueError(f'norm: expected one float32 on {dev}')
+    else:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        workspace = _workspace(workspace, _lib.gdn2_clip_grads_workspace_bytes(), dev)
+    _call(_lib.gdn2_clip_grads, 'gdn2_clip_grads', dev, ptrs, optrs, sizes, types, otypes, len(grads), max_norm,
+          norm.data_ptr(), given, None if given else workspace.data_ptr(),
+          0 if given else workspace.numel() * workspace.element_size())
+    return norm

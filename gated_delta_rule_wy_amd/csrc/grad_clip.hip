@@ -1,0 +1,225 @@
+// The norm over many tensors and their scaling to a largest norm:
+//
+//   norm = sqrt(sum over all elements of g^2),  out = g min(1, max_norm / (norm + 1e-6))
+//
+// Up to kTensors tensors are one launch, their addresses in the kernel's
+// arguments (nothing is copied to the device, so a call can be captured). Every
+// workgroup takes every gridDim-th piece of kPiece elements, whichever tensor it
+// lies in; further launches add to the same partial sums. Squares and sums are
+// fp64 (half the fp32 vector rate, and the loads take longer): no square of a
+// float overflows or vanishes there. The scaling kernel's workgroups
+// each add the partial sums themselves, in one order, so the norm costs no
+// launch of its own and its bits do not depend on timing. The scaling goes from the
+// last piece to the first: what the norm read last is still in the cache.
+// Bound by memory.
+#include "dense_launch.hpp"
+#include "rows.hpp"
+
+#include <algorithm>
+
+namespace gdn2 {
+
+constexpr int kTensors = 64, kThreads = 256, kRounds = 8, kPiece = kThreads * 8 * kRounds;
+
+struct ClipBatch {
+    const void *in[kTensors];
+    void *out[kTensors];
+    int64_t n[kTensors];
+    int32_t first[kTensors];     // its first piece
+    uint64_t in_bf16, out_bf16;  // bits
+    int count, pieces;
+};
+
+// Tensor that piece p lies in: the last one that begins at or before it
+// (tensors without elements are not in a batch).
+static __device__ __forceinline__ int tensor_of(const ClipBatch &b, int p)
+{
+    int lo = 0, hi = b.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (b.first[mid] <= p) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Sum over the workgroup, in every thread, always in the same order.
+static __device__ __forceinline__ double block_sum(double s, double *red)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.;
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; ++i) s += red[i];
+    __syncthreads();
+    return s;
+}
+
+template <typename In> static __device__ __forceinline__ double piece_squares(const In *p, int64_t n)
+{
+    double s = 0.;
+    Pack8<In> x[kRounds];
+    if (n >= kPiece) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) x[r].template load<false, false>(p + (r * kThreads + (int)threadIdx.x) * 8);
+    } else {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int at = (r * kThreads + (int)threadIdx.x) * 8;
+            if (at + 8 <= n) x[r].template load<false, false>(p + at);
+            else x[r].load_some(p + at, (int)n - at);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const double v = (double)x[r].get(i);
+            s += v * v;
+        }
+    return s;
+}
+
+__global__ __launch_bounds__(kThreads) void clip_norm_kernel(ClipBatch b, double *partial, int further)
+{
+    __shared__ double red[kThreads / 64];
+    double s = 0.;
+    for (int p = blockIdx.x; p < b.pieces; p += gridDim.x) {
+        const int t = tensor_of(b, p);
+        const int64_t at = (int64_t)(p - b.first[t]) * kPiece, n = b.n[t] - at;
+        s += (b.in_bf16 >> t) & 1 ? piece_squares((const uint16_t *)b.in[t] + at, n)
+                                  : piece_squares((const float *)b.in[t] + at, n);
+    }
+    s = block_sum(s, red);
+    if (threadIdx.x == 0) partial[blockIdx.x] = (further ? partial[blockIdx.x] : 0.) + s;
+}
+
+static __device__ __forceinline__ float norm_of(const double *partial, int parts, double *red)
+{
+    double s = 0.;
+    for (int i = threadIdx.x; i < parts; i += kThreads) s += partial[i];
+    return (float)sqrt(block_sum(s, red));
+}
+
+__global__ __launch_bounds__(kThreads) void clip_finish_kernel(const double *partial, int parts, float *norm)
+{
+    __shared__ double red[kThreads / 64];
+    const float x = norm_of(partial, parts, red);
+    if (threadIdx.x == 0) *norm = x;
+}
+
+static __device__ __forceinline__ void store_some(uint16_t *p, const float (&x)[8], int n)
+{
+    for (int i = 0; i < n; ++i) store1(p + i, x[i]);
+}
+static __device__ __forceinline__ void store_some(float *p, const float (&x)[8], int n)
+{
+    for (int i = 0; i < n; ++i) store1(p + i, x[i]);
+}
+
+template <typename In, typename Out>
+static __device__ __forceinline__ void piece_scale(const In *p, Out *o, int64_t n, float c)
+{
+    Pack8<In> x[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int at = (r * kThreads + (int)threadIdx.x) * 8;
+        if (at + 8 <= n) x[r].template load<false, false>(p + at);
+        else x[r].load_some(p + at, (int)min(n, (int64_t)kPiece) - at);
+    }
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int at = (r * kThreads + (int)threadIdx.x) * 8;
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[r].get(i) * c;
+        if (at + 8 <= n) store8<false>(o + at, y);
+        else if (at < n) store_some(o + at, y, (int)(n - at));
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipBatch b, const double *partial, int parts,
+                                                              const float *norm_in, float *norm_out, float max_norm)
+{
+    __shared__ double red[kThreads / 64];
+    const float norm = norm_in ? *norm_in : norm_of(partial, parts, red);
+    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+    const double q = (double)max_norm / ((double)norm + 1e-6);
+    const float c = q >= 1. ? 1.f : (float)q;   // (NaN stays)
+    for (int i = blockIdx.x; i < b.pieces; i += gridDim.x) {
+        const int p = b.pieces - 1 - i, t = tensor_of(b, p);
+        const int64_t at = (int64_t)(p - b.first[t]) * kPiece, n = b.n[t] - at;
+        if (c == 1.f && b.in[t] == b.out[t]) continue;   // nothing to change
+        const bool ib = (b.in_bf16 >> t) & 1, ob = (b.out_bf16 >> t) & 1;
+        if (ib) {
+            const uint16_t *x = (const uint16_t *)b.in[t] + at;
+            if (ob) piece_scale(x, (uint16_t *)b.out[t] + at, n, c);
+            else piece_scale(x, (float *)b.out[t] + at, n, c);
+        } else {
+            const float *x = (const float *)b.in[t] + at;
+            if (ob) piece_scale(x, (uint16_t *)b.out[t] + at, n, c);
+            else piece_scale(x, (float *)b.out[t] + at, n, c);
+        }
+    }
+}
+
+// Calls f with each batch of tensors that hold anything, in order or from the last.
+// The pieces of a batch stay below 2^31 (the caller bounds a tensor's size).
+template <typename F> static void for_batches(const ClipArgs &a, bool backwards, F f)
+{
+    ClipBatch b;
+    auto reset = [&] { b.count = b.pieces = 0; b.in_bf16 = b.out_bf16 = 0; };
+    reset();
+    for (int k = 0; k < a.count; ++k) {
+        const int i = backwards ? a.count - 1 - k : k;
+        if (a.sizes[i] == 0) continue;
+        const int64_t pieces = (a.sizes[i] + kPiece - 1) / kPiece;
+        if (b.count == kTensors || b.pieces + pieces > 0x7fff0000LL) {
+            f(b);
+            reset();
+        }
+        b.in[b.count] = a.in[i];
+        b.out[b.count] = a.out ? a.out[i] : nullptr;
+        b.n[b.count] = a.sizes[i];
+        b.first[b.count] = b.pieces;
+        if (a.in_types[i] == 1) b.in_bf16 |= 1ull << b.count;
+        if (a.out && a.out_types[i] == 1) b.out_bf16 |= 1ull << b.count;
+        b.pieces += (int)pieces;
+        ++b.count;
+    }
+    if (b.count) f(b);
+}
+
+hipError_t launch_clip(const ClipArgs &a, hipStream_t st)
+{
+    int64_t most = 0;
+    for_batches(a, false, [&](const ClipBatch &b) { most = std::max<int64_t>(most, b.pieces); });
+    // (no elements: one workgroup adds no parts)
+    const int parts = (int)std::min<int64_t>(most, kClipGrid);
+    if (!a.norm_in) {
+        prof_before("gdn2_grad_norm", st);
+        int further = 0;
+        for_batches(a, false, [&](const ClipBatch &b) {
+            hipLaunchKernelGGL(clip_norm_kernel, dim3(parts), dim3(kThreads), 0, st, b, a.partial, further);
+            further = 1;
+        });
+        prof_after(st);
+    }
+    if (!a.out || parts == 0) {
+        if (!a.norm_in) hipLaunchKernelGGL(clip_finish_kernel, dim3(1), dim3(kThreads), 0, st, a.partial, parts, a.norm_out);
+        return hipGetLastError();
+    }
+    prof_before("gdn2_clip_grads", st);
+    float *norm_out = a.norm_out;
+    for_batches(a, true, [&](const ClipBatch &b) {
+        hipLaunchKernelGGL(clip_scale_kernel, dim3(std::min(b.pieces, kClipGrid)), dim3(kThreads), 0, st, b, a.partial,
+                           parts, a.norm_in, norm_out, a.max_norm);
+        norm_out = nullptr;
+    });
+    prof_after(st);
+    return hipGetLastError();
+}
+
+} // namespace gdn2

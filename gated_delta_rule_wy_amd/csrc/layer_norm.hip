@@ -25,64 +25,11 @@
 // row order, and writes one partial row; a second kernel adds the partial
 // rows in a fixed order (no atomics: the same inputs give the same bits).
 #include "operators_launch.hpp"
-#include "rows.hpp"
+#include "row_parts.hpp"
 
 #include <algorithm>
 
 namespace gdn2 {
-
-template <int TPR> struct RowShape {
-    static constexpr int NT = TPR > 256 ? TPR : 256;   // threads
-    static constexpr int RPB = NT / TPR;               // rows of a workgroup
-};
-
-// How a row of `cols` elements falls into packs of eight: in whole ones; or
-// the last pack reaches back over its neighbour's elements, so that no lane
-// loads element by element; or the row is shorter than a pack.
-enum class Packs { kWhole, kOdd, kFew };
-
-// What a lane holds: pack e of thread p of a row, elements at(e) .. at(e) + 7.
-// mine(e, i): element i counts here (a row's sums take each element once; what
-// a lane holds twice it computes and stores twice, with the same bits).
-template <int TPR, Packs P> struct RowPart {
-    int p, cols;
-    __device__ __forceinline__ int col(int e) const { return (p + e * TPR) * 8; }
-    __device__ __forceinline__ bool any(int e) const { return col(e) < cols; }
-    __device__ __forceinline__ int at(int e) const { return P == Packs::kOdd ? min(col(e), cols - 8) : col(e); }
-    __device__ __forceinline__ bool mine(int e, int i) const
-    {
-        if (P == Packs::kWhole) return any(e);
-        if (P == Packs::kOdd) return at(e) + i >= col(e);
-        return col(e) + i < cols;
-    }
-    template <bool NT = true, typename T> __device__ __forceinline__ void load(Pack8<T> &x, const T *row, int e) const
-    {
-        if constexpr (P == Packs::kOdd) {
-            x.template load<false, NT>(row + at(e));
-        } else if constexpr (P == Packs::kWhole) {
-            x.zero();
-            if (any(e)) x.template load<true, NT>(row + col(e));
-        } else {
-            x.load_some(row + col(e), cols - col(e));
-        }
-    }
-    // its own elements, zeros for others (in whole and few packs those are zeros as loaded)
-    __device__ __forceinline__ float own(float v, int e, int i) const
-    {
-        return P == Packs::kOdd && !mine(e, i) ? 0.f : v;
-    }
-    template <typename T> __device__ __forceinline__ void store(T *row, const float (&x)[8], int e) const
-    {
-        if (!any(e)) return;
-        if constexpr (P == Packs::kFew) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (mine(e, i)) store1(row + col(e) + i, x[i]);
-        } else {
-            store8<P == Packs::kWhole>(row + at(e), x);
-        }
-    }
-};
 
 template <typename In, typename Out, Packs P, int TPR, int E, bool RES>
 __global__ __launch_bounds__((RowShape<TPR>::NT)) void ln_fwd_kernel(
@@ -317,39 +264,6 @@ __global__ __launch_bounds__(1024) void ln_bwd_long_kernel(
 
 // ---- launch ------------------------------------------------------------------
 
-// Calls f with the (packs, TPR, E) that hold a row of `cols` elements in
-// registers, or returns false (the long-row kernels take it). A wave a row as
-// long as its registers hold one (2048 elements; 65536 x 2048 bf16 backward:
-// 137 us, 222 with a workgroup a row).
-template <Packs P> using PacksOf = std::integral_constant<Packs, P>;
-template <typename F> static bool for_row_shape(int cols, F f)
-{
-    auto go = [&](auto t, auto e) {
-        if (cols % 8 == 0) f(PacksOf<Packs::kWhole>{}, t, e);
-        else f(PacksOf<Packs::kOdd>{}, t, e);
-        return true;
-    };
-    if (cols < 8) {
-        f(PacksOf<Packs::kFew>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-        return true;
-    }
-#define GDN2_ROW(T, E) \
-    if (cols <= 8 * T * E) return go(std::integral_constant<int, T>{}, std::integral_constant<int, E>{});
-    GDN2_ROW(8, 1)
-    GDN2_ROW(16, 1)
-    GDN2_ROW(32, 1)
-    GDN2_ROW(64, 1)
-    GDN2_ROW(64, 2)
-    GDN2_ROW(64, 4)
-    GDN2_ROW(256, 2)
-    GDN2_ROW(256, 4)
-    GDN2_ROW(1024, 2)
-#undef GDN2_ROW
-    return false;
-}
-
-static int ln_grid(int64_t rows, int rpb, int most) { return (int)std::min<int64_t>((rows + rpb - 1) / rpb, most); }
-
 template <typename In, typename Out> static void ln_fwd(const LayerNormArgs &a, hipStream_t st)
 {
     const float inv_n = 1.f / (float)a.cols;
@@ -360,11 +274,11 @@ template <typename In, typename Out> static void ln_fwd(const LayerNormArgs &a, 
     const bool held = for_row_shape(a.cols, [&](auto packs, auto t, auto e) {
         constexpr Packs P = decltype(packs)::value;
         constexpr int T = decltype(t)::value, E = decltype(e)::value;
-        const int grid = ln_grid(a.rows, RowShape<T>::RPB, kLnFwdGrid);
+        const int grid = row_grid(a.rows, RowShape<T>::RPB, kLnFwdGrid);
         if (a.residual) args(ln_fwd_kernel<In, Out, P, T, E, true>, grid, RowShape<T>::NT);
         else args(ln_fwd_kernel<In, Out, P, T, E, false>, grid, RowShape<T>::NT);
     });
-    if (!held) args(ln_fwd_long_kernel<In, Out>, ln_grid(a.rows, 1, kLnFwdGrid), 1024);
+    if (!held) args(ln_fwd_long_kernel<In, Out>, row_grid(a.rows, 1, kLnFwdGrid), 1024);
 }
 
 template <typename In, typename Dy> static void ln_bwd(const LayerNormBwdArgs &a, hipStream_t st)
@@ -389,7 +303,7 @@ int ln_bwd_parts(int64_t rows, int cols)
     int rpb = 1;
     (void)for_row_shape(cols, [&](auto, auto t, auto) { rpb = RowShape<decltype(t)::value>::RPB; });
     // (wide rows: fewer parts, so that the partial rows stay within 64 MiB, or 32 rows)
-    return ln_grid(rows, rpb, std::max(32, std::min(kLnBwdGrid, (1 << 23) / cols)));
+    return row_grid(rows, rpb, std::max(32, std::min(kLnBwdGrid, (1 << 23) / cols)));
 }
 
 hipError_t launch_layer_norm_fwd(const LayerNormArgs &a, hipStream_t st)

@@ -1,0 +1,273 @@
+// Gradient of y = act(z) + residual, z = x w^T + bias:
+//
+//   dz = dy act'(z),  dx = dz w,  dw = dz^T x,  db = sum over rows of dz
+//
+// The products (linear_impl.hpp) contract along rows, so what has to be
+// contracted along columns is turned around first: w once for dx, x and dz for dw.
+// The pass that turns dz forms it as well, from dy and the forward's z,
+// with db's partial rows (added by column_sums.hip in a fixed order). These passes
+// are bound by memory.
+//
+// dz is fp32 in that pass, where db takes it, and is rounded to the operands' type for
+// the products: the matrix instructions take no wider bf16 operand, and the
+// gradients that leave are rounded to the same type.
+#include "dense_launch.hpp"
+#include "operators_launch.hpp"
+#include "rows.hpp"
+
+#include <algorithm>
+
+namespace gdn2 {
+
+// act'(z), with e = exp(-|z|) so that nothing cancels for large |z|
+static __device__ __forceinline__ float sigmoid_slope(float u, float &s)
+{
+    const float e = expf(-fabsf(u)), d = 1.f / (1.f + e);
+    s = u < 0.f ? e * d : d;
+    return e * d * d;
+}
+static __device__ __forceinline__ float slope_of(int act, float z)
+{
+    float s;
+    if (act == kActSigmoid) return sigmoid_slope(z, s);
+    if (act == kActSilu) {
+        const float d = sigmoid_slope(z, s);
+        return s + z * d;
+    }
+    if (act == kActGelu) {
+        // (beyond 16 the sigmoid's slope is below the smallest float; z^2 may overflow there)
+        if (fabsf(z) > 16.f) return z > 0.f ? 1.f : 0.f;
+        const float u = 1.5957691216057308f * (z + 0.044715f * z * z * z);
+        const float d = sigmoid_slope(u, s);
+        return s + z * d * 1.5957691216057308f * (1.f + 0.134145f * z * z);
+    }
+    return 1.f;
+}
+
+struct TurnArgs {
+    const void *in;        // [R][C]
+    const void *preact;    // [R][C], type of the outputs; null: in itself is what is turned
+    void *copy;            // [R][Cp] or null
+    void *turned;          // [C][Rp] or null
+    float *partial;        // [gridDim.y][C] column sums, or null
+    int64_t R, Rp;
+    int C, Cp, act;
+};
+
+// Tiles of 64 x 64; a workgroup takes every gridDim.y-th of its 64 columns' tiles.
+// Rp, Cp: R, C rounded up to eight, what is behind R, C filled with zeros.
+template <typename In, typename T> __global__ __launch_bounds__(256) void turn_kernel(TurnArgs a)
+{
+    constexpr int PITCH = 64 + 16 / (int)sizeof(T);
+    __shared__ __attribute__((aligned(16))) T tile[64][PITCH];
+    __shared__ float sums[32][64 + 4];
+    const int p = threadIdx.x % 8, row = threadIdx.x / 8, c0 = blockIdx.x * 64, c = c0 + p * 8;
+    float db[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < a.Rp; r0 += (int64_t)gridDim.y * 64) {
+        Pack8<In> x[2];
+        Pack8<T> z[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r = r0 + h * 32 + row, at = r * a.C + c;
+            const int cnt = r < a.R ? a.C - c : 0;
+            z[h].zero();
+            if (cnt >= 8) {
+                x[h].template load<false, false>((const In *)a.in + at);
+                if (a.preact) z[h].template load<false, false>((const T *)a.preact + at);
+            } else {
+                x[h].load_some((const In *)a.in + at, cnt);
+                if (a.preact) z[h].load_some((const T *)a.preact + at, cnt);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r = r0 + h * 32 + row;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = x[h].get(i);
+                if (a.preact) v[i] *= slope_of(a.act, z[h].get(i));
+                db[i] += v[i];
+            }
+            if (a.copy && r < a.R && c < a.Cp) store8<true>((T *)a.copy + r * a.Cp + c, v);
+            if (a.turned)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) store1(&tile[h * 32 + row][p * 8 + i], v[i]);
+        }
+        if (a.turned) {
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int tc = h * 32 + row;     // column of the tile, row of the outcome
+                const int64_t r = r0 + p * 8;
+                if (c0 + tc < a.C && r < a.Rp) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = in2f<T>(tile[p * 8 + i][tc]);
+                    store8<true>((T *)a.turned + (int64_t)(c0 + tc) * a.Rp + r, v);
+                }
+            }
+            __syncthreads();
+        }
+    }
+    if (a.partial) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[row][p * 8 + i] = db[i];
+        __syncthreads();
+        if (threadIdx.x < 64 && c0 + (int)threadIdx.x < a.C) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x];
+            a.partial[(int64_t)blockIdx.y * a.C + c0 + threadIdx.x] = s;
+        }
+    }
+}
+
+// workgroups along the rows: eight a compute unit in all
+static int turn_rows(int64_t R, int C)
+{
+    const int64_t across = (C + 63) / 64;
+    return (int)std::max<int64_t>(1, std::min((R + 63) / 64, 2048 / across));
+}
+
+static void turn(TurnArgs a, bool in_bf16, bool bf16, const char *name, hipStream_t st)
+{
+    const dim3 grid((a.C + 63) / 64, turn_rows(a.R, a.C));
+    prof_before(name, st);
+    if (bf16) {
+        if (in_bf16) hipLaunchKernelGGL((turn_kernel<uint16_t, uint16_t>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((turn_kernel<float, uint16_t>), grid, dim3(256), 0, st, a);
+    } else {
+        if (in_bf16) hipLaunchKernelGGL((turn_kernel<uint16_t, float>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((turn_kernel<float, float>), grid, dim3(256), 0, st, a);
+    }
+    prof_after(st);
+}
+
+// Where the workspace's parts lie.
+struct BwdLayout {
+    size_t copy = 0, dzt = 0, xt = 0, wt = 0, partial = 0, db = 0, bytes = 0;
+    bool need_copy;
+    int dx_splits = 1, dw_splits = 1;
+};
+static BwdLayout bwd_layout(int64_t M, int N, int K, int act, bool bf16, bool dy_bf16, bool dx, bool dw, bool db)
+{
+    BwdLayout l;
+    const size_t e = bf16 ? 2 : 4;
+    const int64_t Mp = (M + 7) / 8 * 8, Np = (N + 7) / 8 * 8;
+    auto take = [&](size_t n) {
+        const size_t at = l.bytes;
+        l.bytes += (n + 255) / 256 * 256;
+        return at;
+    };
+    // dz where dy is not it, as it stands
+    l.need_copy = dx && (act != kActNone || dy_bf16 != bf16 || N % 8 != 0);
+    if (l.need_copy) l.copy = take((size_t)M * Np * e);
+    if (dw) l.dzt = take((size_t)N * Mp * e);
+    if (dw) l.xt = take((size_t)K * Mp * e);
+    if (dx) l.wt = take((size_t)K * Np * e);
+    size_t part = 0;
+    if (dx && (l.dx_splits = gemm_splits(M, K, Np * e)) > 1) part = (size_t)l.dx_splits * M * K * 4;
+    if (dw && (l.dw_splits = gemm_splits(N, K, Mp * e)) > 1) part = std::max(part, (size_t)l.dw_splits * N * K * 4);
+    if (part) l.partial = take(part);
+    if (db) l.db = take((size_t)turn_rows(M, N) * N * 4);
+    return l;
+}
+
+size_t linear_bwd_workspace(int64_t M, int N, int K, int act, bool bf16, bool dy_bf16, bool dx, bool dw, bool db)
+{
+    return bwd_layout(M, N, K, act, bf16, dy_bf16, dx, dw, db).bytes;
+}
+
+hipError_t launch_linear_bwd(const LinearBwdArgs &a, hipStream_t st)
+{
+    const BwdLayout l = bwd_layout(a.M, a.N, a.K, a.act, a.bf16, a.dy_bf16, a.dx, a.dweight, a.dbias);
+    const Elt elt = a.bf16 ? Elt::kBf16 : Elt::kF32;
+    const size_t e = a.bf16 ? 2 : 4;
+    const int64_t Mp = (a.M + 7) / 8 * 8;
+    const int Np = (a.N + 7) / 8 * 8, Kp = (a.K + 7) / 8 * 8;
+    char *ws = (char *)a.workspace;
+    if (l.need_copy || a.dweight || a.dbias) {
+        TurnArgs t = {};
+        t.in = a.dy;
+        t.preact = a.act == kActNone ? nullptr : a.preact;
+        t.copy = l.need_copy ? ws + l.copy : nullptr;
+        t.turned = a.dweight ? ws + l.dzt : nullptr;
+        t.partial = a.dbias ? (float *)(ws + l.db) : nullptr;
+        t.R = a.M; t.Rp = Mp; t.C = a.N; t.Cp = Np;
+        t.act = a.act;
+        turn(t, a.dy_bf16, a.bf16, "gdn2_linear_bwd_dz", st);
+    }
+    if (a.dx && a.M > 0) {
+        TurnArgs t = {};
+        t.in = a.w;
+        t.turned = ws + l.wt;
+        t.R = a.N; t.Rp = Np; t.C = a.K; t.Cp = Kp;
+        turn(t, a.bf16, a.bf16, "gdn2_linear_bwd_turn", st);
+        GemmArgs m = {};
+        m.x = l.need_copy ? ws + l.copy : a.dy;
+        m.w = ws + l.wt;
+        m.ldx = m.ldw = m.kbytes = (int64_t)Np * e;
+        m.M = a.M; m.N = a.K;
+        m.y = a.dx;
+        m.out_bf16 = a.bf16;
+        m.partial = (float *)(ws + l.partial);
+        m.splits = l.dx_splits;
+        const hipError_t err = launch_gemm(elt, m, "gdn2_linear_bwd_dx", st);
+        if (err != hipSuccess) return err;
+    }
+    if (a.dweight) {
+        TurnArgs t = {};
+        t.in = a.x;
+        t.turned = ws + l.xt;
+        t.R = a.M; t.Rp = Mp; t.C = a.K; t.Cp = Kp;
+        turn(t, a.bf16, a.bf16, "gdn2_linear_bwd_turn", st);
+        GemmArgs m = {};
+        m.x = ws + l.dzt;
+        m.w = ws + l.xt;
+        m.ldx = m.ldw = m.kbytes = Mp * e;
+        m.M = a.N; m.N = a.K;
+        m.y = a.dweight;
+        m.out_bf16 = a.bf16;
+        m.partial = (float *)(ws + l.partial);
+        m.splits = l.dw_splits;
+        const hipError_t err = launch_gemm(elt, m, "gdn2_linear_bwd_dw", st);
+        if (err != hipSuccess) return err;
+    }
+    if (a.dbias) {
+        ColumnSums c = {};
+        c.part[0] = (const float *)(ws + l.db);
+        c.out0[0] = a.dbias;
+        c.n0[0] = a.N;
+        c.parts = turn_rows(a.M, a.N);
+        c.jobs = 1;
+        return launch_column_sums(c, "gdn2_linear_bwd_db", st);
+    }
+    return hipGetLastError();
+}
+
+// ---- the choice of a product's form ---------------------------------------------
+
+int gemm_splits(int64_t M, int64_t N, int64_t kbytes)
+{
+    auto tiles = [&](int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
+    const int64_t steps = (kbytes + 127) / 128, big = tiles(256), small = tiles(128);
+    if (M == 0 || big >= 192) return 1;
+    // one part a compute unit, each of 16 steps (8 of the smaller tiles) at least
+    const int64_t s = std::min((256 + big - 1) / big, steps / 16);
+    if (s >= 1 && big * s >= 192) return (int)s;
+    if (M <= 64 || (tiles(64) <= 512 && steps <= 64)) return 1;   // (few tiles: the waves share the contraction)
+    return (int)std::max<int64_t>(1, std::min((256 + small - 1) / small, steps / 8));
+}
+
+hipError_t launch_gemm(Elt e, const GemmArgs &a, const char *name, hipStream_t st)
+{
+    if (a.M == 0) return hipSuccess;
+    prof_before(name, st);
+    const hipError_t err = e == Elt::kBf16 ? launch_gemm_bf16(a, st) : e == Elt::kF32 ? launch_gemm_f32(a, st)
+                                                                                     : launch_gemm_e4m3(a, st);
+    prof_after(st);
+    return err;
+}
+
+} // namespace gdn2

@@ -1,43 +1,12 @@
 // C ABI of the operators around the mixer (declared in include/gdn2.h): argument
 // validation and dispatch to the kernels. Nothing is enqueued unless every check
 // passes.
-#include "api_common.hpp"
+#include "operators_checks.hpp"
 #include "operators_launch.hpp"
-
-#include <initializer_list>
 
 using namespace gdn2;
 
 extern "C" {
-
-static hipStream_t stream() { return (hipStream_t)gdn2_get_stream(); }
-
-static bool dtype_ok(int t) { return t == GDN2_F32 || t == GDN2_BF16; }
-
-// Whether an output is an input's own memory (partial overlaps are the caller's).
-using Ptrs = std::initializer_list<const void *>;
-static bool same_memory(Ptrs outs, Ptrs ins)
-{
-    for (const void *o : outs)
-        for (const void *i : ins)
-            if (o && o == i) return true;
-    return false;
-}
-
-// Whether two outputs are one.
-static bool twice(Ptrs outs)
-{
-    for (auto o = outs.begin(); o != outs.end(); ++o)
-        for (auto p = outs.begin(); p != o; ++p)
-            if (*o && *o == *p) return true;
-    return false;
-}
-
-// Sizes whose launch would have too many threads are found where it is laid out.
-static int launch_status(hipError_t err)
-{
-    return err == hipSuccess ? GDN2_OK : err == hipErrorInvalidConfiguration ? GDN2_ERR_UNSUPPORTED : GDN2_ERR_HIP;
-}
 
 // Sizes shared by the recurrence on slots and the prologue.
 static int serve_check(int B, int T, int N, int H, int HK, int dk, int dv, int in_dtype, int varlen)

@@ -54,7 +54,8 @@ typedef enum {
  * side; a value that is not one of these gives GDN2_ERR_INVALID. */
 typedef enum {
     GDN2_F32 = 0,
-    GDN2_BF16 = 1
+    GDN2_BF16 = 1,
+    GDN2_E4M3 = 2             /* 8 bits, only where an entry point names it   */
 } gdn2_dtype;
 
 /*
@@ -497,6 +498,116 @@ size_t gdn2_layer_norm_bwd_workspace_bytes(int64_t rows, int cols);
 int gdn2_layer_norm_bwd(const void *dy, const void *h, const float *weight, const void *dsum, void *dh, float *dweight,
                         float *dbias, int64_t rows, int cols, float eps, int in_dtype, int out_dtype, void *workspace,
                         size_t workspace_bytes);
+
+/*
+ * ---- The layer's projections, and their gradient ------------------------------
+ *
+ * A linear layer with what follows it (the projections to q, k, v, the gate
+ * logits with their sigmoid, out_proj with the residual's addition; aifetchly,
+ * "Gated DeltaNet-2 Guide", "End-to-End PyTorch Implementation"):
+ *   z = x_scale[row] weight_scale[n] sum_k x[row, k] weight[n, k] + bias[n]
+ *   y = act(z) + residual
+ *
+ *   x            [rows, in_features] in_dtype (GDN2_F32, GDN2_BF16 or GDN2_E4M3)
+ *   weight       [out_features, in_features] in_dtype
+ *   x_scale      [rows] float, weight_scale [out_features] float: with
+ *                GDN2_E4M3, and only then (gdn2_rms_norm_fwd writes such rows)
+ *   bias         [out_features] float, or NULL (none)
+ *   residual     [rows, out_features] out_dtype, or NULL (none); y may be it
+ *   y            [rows, out_features] out_dtype (GDN2_F32 or GDN2_BF16)
+ *   preact       [rows, out_features] in_dtype, or NULL: receives z, rounded
+ *                (not with GDN2_E4M3): what the gradient of an activation takes
+ * act: none, sigmoid, silu z sigmoid(z), or gelu in its tanh form
+ *   0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))).
+ * e4m3 is the 8-bit float with 4 exponent and 3 mantissa bits, no infinities
+ * and largest value 448. Products are exact and sums fp32, in a fixed order.
+ * Otherwise no output overlaps an input or another output (GDN2_ERR_INVALID
+ * where two pointers are one; partial overlaps are not checked).
+ *
+ * gdn2_linear_bwd: from dy = dL/dy (dy_dtype: the forward's out_dtype) the
+ * gradients dx, dweight (in_dtype, shaped like x and weight) and dbias (float);
+ * each may be NULL, not all of them. The residual's gradient is dy itself.
+ * preact: the z that the forward wrote (NULL without an activation). dz =
+ * dy act'(z) is rounded to in_dtype for the products; dbias sums it unrounded.
+ * x may be NULL without dweight, weight without dx. in_dtype: GDN2_F32 or
+ * GDN2_BF16. No output, nor the workspace, may overlap an input or another
+ * output. workspace: gdn2_linear_bwd_workspace_bytes(...) of device memory.
+ *
+ * rows >= 0; 1 <= in_features, out_features <= GDN2_LINEAR_MAX_FEATURES.
+ * GDN2_ERR_UNSUPPORTED for products of two of the three sizes of about 2^37
+ * and more. Pointers are 16-byte aligned; the sizes may be any number
+ * (in_features in whole 16 bytes and out_features in whole eights are faster).
+ */
+typedef enum {
+    GDN2_ACT_NONE = 0,
+    GDN2_ACT_SIGMOID = 1,
+    GDN2_ACT_SILU = 2,
+    GDN2_ACT_GELU_TANH = 3
+} gdn2_activation;
+#define GDN2_LINEAR_MAX_FEATURES (1 << 20)
+int gdn2_linear_fwd(const void *x, const void *weight, const float *bias, const void *residual, const float *x_scale,
+                    const float *weight_scale, void *y, void *preact, int64_t rows, int in_features, int out_features,
+                    int activation, int in_dtype, int out_dtype);
+size_t gdn2_linear_bwd_workspace_bytes(int64_t rows, int in_features, int out_features, int activation, int in_dtype,
+                                       int dy_dtype, int need_dx, int need_dweight, int need_dbias);
+int gdn2_linear_bwd(const void *dy, const void *x, const void *weight, const void *preact, void *dx, void *dweight,
+                    float *dbias, int64_t rows, int in_features, int out_features, int activation, int in_dtype,
+                    int dy_dtype, void *workspace, size_t workspace_bytes);
+
+/*
+ * ---- RMS norm of x + residual, and its gradient --------------------------------
+ *
+ * The norm before a layer's projections, over rows of `cols` elements:
+ *   h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight
+ *
+ *   x, residual, sum, weight   as in gdn2_layer_norm_fwd
+ *   y            [rows, cols] out_dtype: GDN2_F32, GDN2_BF16, or GDN2_E4M3 with
+ *   scale        [rows] float (NULL otherwise): max |y| / 448 of the row, at
+ *                least 2^-126; y then holds y / scale, to nearest even, which
+ *                gdn2_linear_fwd takes with this x_scale
+ * y (same type) and sum may each be x or residual itself, but must not overlap
+ * an input otherwise, nor each other (GDN2_ERR_INVALID where they are one). The
+ * squares of a row are added in fp32: above about 1e19 their sum is infinite.
+ *
+ * gdn2_rms_norm_bwd: as gdn2_layer_norm_bwd, without a bias; dy is dL/dy in
+ * out_dtype, GDN2_F32 or GDN2_BF16.
+ * workspace: gdn2_rms_norm_bwd_workspace_bytes(...) of device memory.
+ * Sizes, alignment and errors as in gdn2_layer_norm_fwd.
+ */
+int gdn2_rms_norm_fwd(const void *x, const void *residual, const float *weight, void *y, float *scale, void *sum,
+                      int64_t rows, int cols, float eps, int in_dtype, int out_dtype);
+size_t gdn2_rms_norm_bwd_workspace_bytes(int64_t rows, int cols);
+int gdn2_rms_norm_bwd(const void *dy, const void *h, const float *weight, const void *dsum, void *dh, float *dweight,
+                      int64_t rows, int cols, float eps, int in_dtype, int out_dtype, void *workspace,
+                      size_t workspace_bytes);
+
+/*
+ * ---- The norm over many gradients, and their clipping ---------------------------
+ *
+ *   norm = sqrt(sum of g^2 over all elements of all tensors)
+ *   out[i] = grads[i] * min(1, max_norm / (norm + 1e-6))
+ *
+ *   grads, out   host arrays of `count` device pointers; sizes: host array of
+ *                element counts (0 is allowed, its pointers are then unused);
+ *                dtypes, out_dtypes: host arrays of GDN2_F32 / GDN2_BF16. All are
+ *                read before the call returns.
+ *   norm         [1] float on the device: written, or, where norm_given is not
+ *                0, read (a norm over several devices' parts, say)
+ *   workspace    gdn2_clip_grads_workspace_bytes() of device memory (NULL is
+ *                allowed with norm_given)
+ * out[i] may be grads[i] itself with the same dtype (nothing is written there when nothing
+ * is to be scaled); otherwise no out[i] may overlap any grads[j] or out[j]
+ * (GDN2_ERR_INVALID; checked over their whole length). Tensors lie at any
+ * multiple of their element's size. Squares and their sums are fp64, in a fixed
+ * order. An infinite norm makes finite gradients 0 and infinite ones NaN; a NaN
+ * one makes all of them NaN. 0 <= max_norm, finite.
+ */
+size_t gdn2_clip_grads_workspace_bytes(void);
+int gdn2_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int count, float *norm,
+                   void *workspace, size_t workspace_bytes);
+int gdn2_clip_grads(const void *const *grads, void *const *out, const int64_t *sizes, const int32_t *dtypes,
+                    const int32_t *out_dtypes, int count, float max_norm, float *norm, int norm_given, void *workspace,
+                    size_t workspace_bytes);
 
 /*
  * Per-kernel timing, for measurement tools (not needed for computing).
