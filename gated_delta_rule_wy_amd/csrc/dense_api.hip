@@ -17,7 +17,7 @@ static int linear_check(int64_t rows, int in_features, int out_features, int act
 {
     if (rows < 0 || in_features < 1 || out_features < 1) return GDN2_ERR_INVALID;
     if (activation < GDN2_ACT_NONE || activation > GDN2_ACT_GELU_TANH) return GDN2_ERR_INVALID;
-    if (in_features > GDN2_LINEAR_MAX_FEATURES || out_features > GDN2_LINEAR_MAX_FEATURES || rows > 0x7fffffffLL)
+    if (in_features > GDN2_LINEAR_MAX_FEATURES || out_features > GDN2_LINEAR_MAX_FEATURES || rows > 0x7fff0000LL)
         return GDN2_ERR_UNSUPPORTED;
     // (one launch: tiles of 128 x 128, 512 threads each)
     auto tiles = [](int64_t a, int64_t b) { return ((a + 127) / 128) * ((b + 127) / 128) > 0x7fffffLL; };
@@ -70,7 +70,7 @@ size_t gdn2_linear_bwd_workspace_bytes(int64_t rows, int in_features, int out_fe
                                        int dy_dtype, int need_dx, int need_dweight, int need_dbias)
 {
     if (linear_check(rows, in_features, out_features, activation) != GDN2_OK) return 0;
-    if (!dtype_ok(in_dtype) || !dtype_ok(dy_dtype)) return 0;
+    if (!dtype_ok(in_dtype) || !dtype_ok(dy_dtype) || rows > GDN2_LINEAR_BWD_MAX_ROWS) return 0;
     const size_t need = linear_bwd_workspace(rows, out_features, in_features, activation, in_dtype == GDN2_BF16,
                                              dy_dtype == GDN2_BF16, need_dx, need_dweight, need_dbias);
     return need > 0 ? need : 256;
@@ -84,6 +84,7 @@ int gdn2_linear_bwd(const void *dy, const void *x, const void *weight, const voi
     if (st != GDN2_OK) return st;
     if (!dtype_ok(in_dtype) || !dtype_ok(dy_dtype)) return GDN2_ERR_INVALID;
     if (!dx && !dweight && !dbias) return GDN2_ERR_INVALID;
+    if (rows > GDN2_LINEAR_BWD_MAX_ROWS) return GDN2_ERR_UNSUPPORTED;
     if (rows > 0 && (!dy || (dweight && !x) || (dx && !weight) || (activation != GDN2_ACT_NONE && !preact)))
         return GDN2_ERR_INVALID;
     const void *ptrs[] = {dy, x, weight, preact, dx, dweight, dbias, workspace};

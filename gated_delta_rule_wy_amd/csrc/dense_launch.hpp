@@ -66,7 +66,10 @@ struct GemmArgs {
     void *y, *preact;            // [M][N]; preact (bf16 where y's operands are, else fp32): or null
     int act;
     bool out_bf16, preact_bf16;
-    float *partial;              // splits > 1: [splits][M][N]
+    // splits > 1 (rows at whole 16 bytes only): partial [splits][M][ldp]; ldp: N rounded up to eight, and
+    // so many rows of w can be read
+    float *partial;
+    int64_t ldp;
     int splits;
 };
 // parts that the contraction is split into, for a product whose partial sums may be kept in a workspace

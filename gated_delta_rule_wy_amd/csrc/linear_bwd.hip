@@ -154,7 +154,7 @@ static BwdLayout bwd_layout(int64_t M, int N, int K, int act, bool bf16, bool dy
 {
     BwdLayout l;
     const size_t e = bf16 ? 2 : 4;
-    const int64_t Mp = (M + 7) / 8 * 8, Np = (N + 7) / 8 * 8;
+    const int64_t Mp = (M + 7) / 8 * 8, Np = (N + 7) / 8 * 8, Kp = (K + 7) / 8 * 8;
     auto take = [&](size_t n) {
         const size_t at = l.bytes;
         l.bytes += (n + 255) / 256 * 256;
@@ -164,11 +164,11 @@ static BwdLayout bwd_layout(int64_t M, int N, int K, int act, bool bf16, bool dy
     l.need_copy = dx && (act != kActNone || dy_bf16 != bf16 || N % 8 != 0);
     if (l.need_copy) l.copy = take((size_t)M * Np * e);
     if (dw) l.dzt = take((size_t)N * Mp * e);
-    if (dw) l.xt = take((size_t)K * Mp * e);
-    if (dx) l.wt = take((size_t)K * Np * e);
+    if (dw) l.xt = take((size_t)Kp * Mp * e);
+    if (dx) l.wt = take((size_t)Kp * Np * e);
     size_t part = 0;
-    if (dx && (l.dx_splits = gemm_splits(M, K, Np * e)) > 1) part = (size_t)l.dx_splits * M * K * 4;
-    if (dw && (l.dw_splits = gemm_splits(N, K, Mp * e)) > 1) part = std::max(part, (size_t)l.dw_splits * N * K * 4);
+    if (dx && (l.dx_splits = gemm_splits(M, K, Np * e)) > 1) part = (size_t)l.dx_splits * M * Kp * 4;
+    if (dw && (l.dw_splits = gemm_splits(N, K, Mp * e)) > 1) part = std::max(part, (size_t)l.dw_splits * N * Kp * 4);
     if (part) l.partial = take(part);
     if (db) l.db = take((size_t)turn_rows(M, N) * N * 4);
     return l;
@@ -212,6 +212,7 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a, hipStream_t st)
         m.y = a.dx;
         m.out_bf16 = a.bf16;
         m.partial = (float *)(ws + l.partial);
+        m.ldp = Kp;
         m.splits = l.dx_splits;
         const hipError_t err = launch_gemm(elt, m, "gdn2_linear_bwd_dx", st);
         if (err != hipSuccess) return err;
@@ -230,6 +231,7 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a, hipStream_t st)
         m.y = a.dweight;
         m.out_bf16 = a.bf16;
         m.partial = (float *)(ws + l.partial);
+        m.ldp = Kp;
         m.splits = l.dw_splits;
         const hipError_t err = launch_gemm(elt, m, "gdn2_linear_bwd_dw", st);
         if (err != hipSuccess) return err;

@@ -23,6 +23,9 @@ typedef u4 u4_byte __attribute__((aligned(1)));
 
 constexpr int kStep = 128;   // bytes of a row a step
 
+#define GDN2_INLINE __attribute__((always_inline))
+static __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // Products of two chunks of 16 w rows with two of 16 x rows (16 x 16 sums).
 template <Elt T> struct Mm;
 template <> struct Mm<Elt::kBf16> {
@@ -85,8 +88,12 @@ template <Elt T, bool ODD> static __device__ __forceinline__ u4 load_chunk(const
 
 // ---- the epilogue ----------------------------------------------------------------
 
-// 1 / (1 + exp(-z)): exp overflows to infinity and its reciprocal to 0
-static __device__ __forceinline__ float sigmoid_of(float z) { return __builtin_amdgcn_rcpf(1.f + expf(-z)); }
+// 1 / (1 + exp(-z)); exp overflows to infinity, whose reciprocal is 0. The exponent's
+// product with log2 e is rounded once, which is to z as one more rounding of its own.
+static __device__ __forceinline__ float sigmoid_of(float z)
+{
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+}
 
 template <int ACT> static __device__ __forceinline__ float act_of(float z)
 {
@@ -142,45 +149,42 @@ static __device__ __forceinline__ void put8(void *p, bool bf16, int64_t at, int 
     else put8((float *)p + at, n, x);
 }
 
-// The steps of the epilogue for eight sums of row m, columns n .. n + 7 (cnt of
-// them in the row): up to z, and from act(z) on.
-static __device__ __forceinline__ void to_preact(const GemmArgs &a, int64_t m, int64_t n, int cnt, float (&v)[8])
-{
-    float s[8];
-    if (a.sw) {
-        const float sx = a.sx[m];
-        get8(a.sw + n, cnt, s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= sx * s[i];
+// The epilogue of eight sums of row m, columns n .. n + 7 (cnt of them in the
+// row): what it reads, on its way before the sums are there, and then y.
+struct Finish8 {
+    float sw[8], bias[8], res[8], sx;
+    __device__ __forceinline__ void load(const GemmArgs &a, int64_t m, int64_t n, int cnt)
+    {
+        if (a.sw) {
+            sx = a.sx[m];
+            get8(a.sw + n, cnt, sw);
+        }
+        if (a.bias) get8(a.bias + n, cnt, bias);
+        if (a.residual) {
+            if (a.out_bf16) get8((const uint16_t *)a.residual + m * a.N + n, cnt, res);
+            else get8((const float *)a.residual + m * a.N + n, cnt, res);
+        }
     }
-    if (a.bias) {
-        get8(a.bias + n, cnt, s);
+    __device__ __forceinline__ void store(const GemmArgs &a, int64_t m, int64_t n, int cnt, float (&v)[8]) const
+    {
+        const int64_t at = m * a.N + n;
+        if (a.sw)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += s[i];
+            for (int i = 0; i < 8; ++i) v[i] *= sx * sw[i];
+        if (a.bias)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += bias[i];
+        if (a.preact) put8(a.preact, a.preact_bf16, at, cnt, v);
+        with_act(a.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_of<decltype(act)::value>(v[i]);
+        });
+        if (a.residual)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += res[i];
+        put8(a.y, a.out_bf16, at, cnt, v);
     }
-    if (a.preact) put8(a.preact, a.preact_bf16, m * a.N + n, cnt, v);
-}
-static __device__ __forceinline__ void to_output(const GemmArgs &a, int64_t m, int64_t n, int cnt, float (&v)[8])
-{
-    const int64_t at = m * a.N + n;
-    if (a.residual) {
-        float s[8];
-        if (a.out_bf16) get8((const uint16_t *)a.residual + at, cnt, s);
-        else get8((const float *)a.residual + at, cnt, s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += s[i];
-    }
-    put8(a.y, a.out_bf16, at, cnt, v);
-}
-static __device__ __forceinline__ void finish8(const GemmArgs &a, int64_t m, int64_t n, int cnt, float (&v)[8])
-{
-    to_preact(a, m, n, cnt, v);
-    with_act(a.act, [&](auto act) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_of<decltype(act)::value>(v[i]);
-    });
-    to_output(a, m, n, cnt, v);
-}
+};
 
 // ---- few tiles: every wave a part of the contraction -----------------------------
 //
@@ -239,6 +243,9 @@ template <Elt T, int MB, int NB, bool ODD> __global__ __launch_bounds__(kWaves *
             const int row = e / (NB * 2), col = e % (NB * 2) * 8;
             const int64_t m = m0 + q * MR * 16 + row, n = n0 + col;
             if (m < a.M && n < a.N) {
+                const int cnt = (int)min((int64_t)8, a.N - n);
+                Finish8 fin;
+                fin.load(a, m, n, cnt);
                 float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < kWaves; ++i)
@@ -248,99 +255,416 @@ template <Elt T, int MB, int NB, bool ODD> __global__ __launch_bounds__(kWaves *
 #pragma unroll
                         for (int c = 0; c < 4; ++c) v[h * 4 + c] += s[c];
                     }
-                finish8(a, m, n, (int)min((int64_t)8, a.N - n), v);
+                fin.store(a, m, n, cnt, v);
             }
         }
     }
 }
 
 // ---- many tiles -------------------------------------------------------------------
-//
-// A workgroup of WM x WN waves owns BM rows of x and BN of w. Each step's
-// chunks lie in LDS, two steps at a time: while the waves multiply one, the next
-// is on its way, without a register in between (ODD: through registers, since
-// the direct way takes whole aligned chunks).
-//
-// A fragment's 16 rows, 128 bytes apart, would fall on the same banks; so chunk c
-// of row i lies at position c ^ swap(i), and neighbouring pairs of rows that are
-// read together differ in it.
-//
-// Which of w's rows an instruction takes as its 16 is free, too: block j of a
-// pair takes rows 8 t + 4 j + (0..3), t = 0..3, of the pair's 32, so that
-// a lane's sums of both blocks are eight neighbours of a row of y.
-static __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
-// (rows r, r + 1 share one: a row is half as long as all banks together)
-static __device__ __forceinline__ int swap_x(int row) { return (row >> 1) & 7; }
-static __device__ __forceinline__ int swap_w(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
+typedef float f16v __attribute__((ext_vector_type(16)));
 
-template <Elt T, int BM, int BN, int WM, int WN, bool ODD>
-__global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(GemmArgs a, int tm, int tn)
+// Products of two chunks of 32 w rows with two of 32 x rows (32 x 32 sums). Lane
+// l has row l % 32 and, of 64 bytes, chunks l / 32 and 2 + l / 32.
+template <Elt T> static __device__ __forceinline__ f16v mma32(const u4 (&w)[2], const u4 (&x)[2], f16v c)
 {
-    constexpr int NW = WM * WN, MB = BM / WM / 16, NB = BN / WN / 16;   // waves; blocks of 16 rows a wave
+    if constexpr (T == Elt::kBf16) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, w[j]), __builtin_bit_cast(b8, x[j]), c, 0, 0, 0);
+    } else if constexpr (T == Elt::kF32) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w[j][i]), __uint_as_float(x[j][i]), c, 0, 0, 0);
+    } else {
+        struct P { u4 a[2]; };
+        const P pw = {{w[0], w[1]}}, px = {{x[0], x[1]}};
+        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_bit_cast(i8v, pw), __builtin_bit_cast(i8v, px), c, 0, 0, 0,
+                                                            0x7f7f7f7f, 0, 0x7f7f7f7f);
+    }
+    return c;
+}
+
+// Rows of 128 bytes in LDS: a fragment's rows would fall on the same banks, so
+// chunk c of row r lies at position c ^ swap(r). (Rows 2 i, 2 i + 1 share one: a row is
+// half as long as all banks together.)
+static __device__ __forceinline__ int swap_of(int row) { return (row >> 1) & 7; }
+
+// A workgroup of WM x WN waves owns BM rows of x and BN of w at a time, a wave 32
+// MB x 32 NB sums. Each step's chunks lie in LDS, two steps' at a time, brought
+// there without a register in between.
+//
+// A step is two halves of 64 bytes. A wave multiplies the first while it reads the
+// second into registers; then (every wave has read all of the step, and its
+// own part of the next one has landed) a barrier, after which the step's LDS takes the one after
+// next, and the wave multiplies the second half while it reads the first of
+// the next. So the matrix cores wait neither at the barrier nor for LDS, and a
+// step's loads have a whole step to land.
+//
+// Workgroups stay and go through the tiles; the last two steps of a tile bring
+// the first two of the next, so the sums' way to memory overlaps with them.
+// The kernel's first argument, where it lies in memory.
+static __device__ __forceinline__ GemmArgs arguments()
+{
+    auto p = (const __attribute__((address_space(4))) GemmArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const GemmArgs *)p;
+}
+
+// A buffer descriptor from `at` bytes into `base` to its end at `end` bytes: what is
+// read beyond arrives as zeros, what is written there is dropped. Offsets are
+// whole in the vector operand, which the bounds are checked against; kBeyond is
+// outside always.
+constexpr uint32_t kBeyond = 0xFFFFFF80u;   // (and 16 bytes on)
+static __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void *base, int64_t at, int64_t end)
+{
+    const uint32_t left = (end - at) >> 32 ? 0xFFFFFF00u : (uint32_t)(end - at);
+    return __builtin_amdgcn_make_buffer_rsrc((char *)const_cast<void *>(base) + at, (short)0, (int)left, 0x00020000);
+}
+
+// The epilogue of a wave's blocks, from row mw and column nw of y on. Each 32 x 32
+// block is turned through the wave's own piece of LDS, `mine`, so that four lanes have
+// 32 neighbours of a row. What is read is asked for before the writes of the blocks
+// before: both come back in order, and a read behind a write would wait for it.
+// PART: the sums alone, to the partial sums that begin at element `part`.
+template <Elt T, typename Out, bool PART, int MB, int NB>
+static __device__ __forceinline__ void finish_blocks(const GemmArgs &e, int64_t part, int mw, int nw, int lane, char *mine,
+                                                     const f16v (&acc)[NB][MB])
+{
+    constexpr int RS = sizeof(Out) / 2;   // 16-byte pieces of eight elements
+    asm volatile("" : "+v"(lane));
+    const int er = lane & 31, eh = lane >> 5, c8 = (lane & 3) * 8, row = lane >> 2;
+    const uint32_t N = (uint32_t)e.N;
+    const int64_t at = (int64_t)mw * e.N + nw, end = e.M * e.N;
+    void *dst = PART ? (void *)(e.partial + part) : e.y;
+    const auto to = buffer_at(dst, at * (int)sizeof(Out), end * (int)sizeof(Out));
+    const auto from = buffer_at(e.residual ? e.residual : dst, at * (int)sizeof(Out), end * (int)sizeof(Out));
+    const uint32_t first = (uint32_t)row * N + c8;
+    // element 8 c8 of row t of block (j, i), in bytes of `size` an element
+    auto offset = [&](int j, int i, int t, int size) GDN2_INLINE {
+        return (int)(nw + j * 32 + c8 < (int)N ? (first + ((i * 32 + t * 16) * N + j * 32)) * size : kBeyond);
+    };
+    struct Column { u4 s[2], b[2]; } col[2];
+    u4 old[2][2][RS];   // [block % 2][t]
+    float sx[MB][2];
+    auto ahead = [&](int b) GDN2_INLINE {
+        const int j = b / MB, i = b % MB;
+        if (i == 0) {
+            if (e.sw) {
+                const auto p = buffer_at(e.sw, (int64_t)nw * 4, e.N * 4);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    col[j & 1].s[k] = __builtin_amdgcn_raw_buffer_load_b128(p, (j * 32 + c8 + k * 4) * 4, 0, 0);
+            }
+            if (e.bias) {
+                const auto p = buffer_at(e.bias, (int64_t)nw * 4, e.N * 4);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    col[j & 1].b[k] = __builtin_amdgcn_raw_buffer_load_b128(p, (j * 32 + c8 + k * 4) * 4, 0, 0);
+            }
+        }
+        if (e.residual)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int k = 0; k < RS; ++k)
+                    old[b & 1][t][k] = __builtin_amdgcn_raw_buffer_load_b128(from, offset(j, i, t, sizeof(Out)) + k * 16, 0, 0);
+    };
+    if constexpr (!PART) {
+        if (e.sw) {
+            const auto p = buffer_at(e.sx, (int64_t)mw * 4, e.M * 4);
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    sx[i][t] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(p, (i * 32 + t * 16 + row) * 4, 0, 0));
+        }
+        ahead(0);
+    }
+#pragma unroll
+    for (int b = 0; b < NB * MB; ++b) {
+        const int j = b / MB, i = b % MB;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<f4 *>(mine + er * 128 + (((c * 2 + eh) ^ swap_of(er)) << 4)) =
+                (f4){acc[j][i][c * 4], acc[j][i][c * 4 + 1], acc[j][i][c * 4 + 2], acc[j][i][c * 4 + 3]};
+        if (!PART && b + 1 < NB * MB) ahead(b + 1);
+        __builtin_amdgcn_wave_barrier();
+        float v[2][8];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f4 x = *reinterpret_cast<const f4 *>(mine + (t * 16 + row) * 128 +
+                                                           ((((lane & 3) * 2 + k) ^ swap_of(t * 16 + row)) << 4));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[t][k * 4 + c] = x[c];
+            }
+        __builtin_amdgcn_wave_barrier();
+        auto store = [&](__amdgpu_buffer_rsrc_t p, auto type) GDN2_INLINE {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int o = offset(j, i, t, sizeof(type));
+                if constexpr (sizeof(type) == 2) {
+                    const u4 x = {bf16x2(v[t][0], v[t][1]), bf16x2(v[t][2], v[t][3]), bf16x2(v[t][4], v[t][5]), bf16x2(v[t][6], v[t][7])};
+                    __builtin_amdgcn_raw_buffer_store_b128(x, p, o, 0, 0);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const f4 x = {v[t][k * 4], v[t][k * 4 + 1], v[t][k * 4 + 2], v[t][k * 4 + 3]};
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), p, o + k * 16, 0, 0);
+                    }
+                }
+            }
+        };
+        if constexpr (!PART) {
+            const Column &q = col[j & 1];
+            if (e.sw)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[t][c] *= sx[i][t] * __uint_as_float(q.s[c >> 2][c & 3]);
+            if (e.bias)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[t][c] += __uint_as_float(q.b[c >> 2][c & 3]);
+            if constexpr (T != Elt::kE4m3)
+                if (e.preact) {
+                    using Z = std::conditional_t<T == Elt::kBf16, uint16_t, float>;
+                    store(buffer_at(e.preact, at * (int)sizeof(Z), end * (int)sizeof(Z)), Z(0));
+                }
+            with_act(e.act, [&](auto act) GDN2_INLINE {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[t][c] = act_of<decltype(act)::value>(v[t][c]);
+            });
+            if (e.residual)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const u4 (&o)[RS] = old[b & 1][t];
+                        v[t][c] += sizeof(Out) == 4 ? __uint_as_float(o[(c >> 2) % RS][c & 3])
+                                   : c & 1          ? __uint_as_float(o[0][c >> 1] & 0xFFFF0000u)
+                                                    : __uint_as_float(o[0][c >> 1] << 16);
+                    }
+        }
+        store(to, Out(0));
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// Waits for what this wave has under way from memory to LDS (a barrier alone does not).
+static __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <Elt T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2))) void gemm_tile_kernel(GemmArgs a, int tm,
+                                                                                                       int tn)
+{
+    constexpr int NW = WM * WN, MB = BM / WM / 32, NB = BN / WN / 32;
     constexpr int RX = BM / 8 / NW, RW = BN / 8 / NW;                   // groups of 8 rows each wave brings
     constexpr int BUF = (BM + BN) * kStep;
-    static_assert(RX * 8 * NW == BM && RW * 8 * NW == BN && NB % 2 == 0, "whole groups a wave, whole pairs");
-    static_assert(NW % 4 == 0, "a wave's groups keep their place in 32 rows");
+    static_assert(RX * 8 * NW == BM && RW * 8 * NW == BN && NW % 2 == 0, "whole groups a wave, in one half of 16 rows");
+    __shared__ __attribute__((aligned(1024))) char lds[2 * BUF + NW * 4096];
+    const int lane = threadIdx.x & 63, wv = wave_id();
+    const int wm = wv % WM, wn = wv / WM;
+    const int steps = (int)((a.kbytes + kStep - 1) / kStep);
+
+    // Units (tiles of each part of the contraction) in an order that gives
+    // neighbouring ones to one XCD (workgroups go round the eight of them)
+    const int all = tm * tn * a.splits, xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
+    const int first = uniform(xcd * (all >> 3) + min(xcd, all & 7)), count = (all >> 3) + (xcd < (all & 7) ? 1 : 0);
+    struct Unit { int m0, n0, part, s0, s1; };
+    auto unit_of = [&](int j) GDN2_INLINE {
+        const int u = first + j, tiles = tm * tn, part = a.splits > 1 ? u / tiles : 0, tile = u - part * tiles;
+        // bands of four tiles of x
+        const int band = tile / (4 * tn), inb = tile - band * 4 * tn, bm = min(4, tm - band * 4), col = inb / bm;
+        return Unit{uniform((band * 4 + inb - col * bm) * BM), uniform(col * BN), uniform(part),
+                    uniform((int)((unsigned)steps * part / a.splits)), uniform((int)((unsigned)steps * (part + 1) / a.splits))};
+    };
+
+    // What a lane brings: of every NW-th group of 8 rows, row lane / 8 and the
+    // chunk that belongs at position lane % 8. Reads go through buffer descriptors that
+    // end with the operand, and what lies beyond an end arrives as zeros: rows behind the
+    // last one, and chunks behind a row's end, whose offset is made too large.
+    const uint32_t gx = (uint32_t)(NW * 8) * (uint32_t)a.ldx, gw = (uint32_t)(NW * 8) * (uint32_t)a.ldw;
+    uint32_t vx, vw;               // bytes from the step's first
+    int cof, ox, ow;               // its chunk in a row; in LDS: this lane's rows of x and w, at its chunk
+    auto place = [&]() GDN2_INLINE {
+        // (lane from where the compiler cannot see it, here and in the epilogue: what is made
+        // of it would otherwise be kept in registers through both)
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        const int grow = l >> 3;
+        cof = ((l & 7) ^ swap_of((wv & 1) * 8 + grow)) * 16;
+        vx = (uint32_t)(wv * 8 + grow) * (uint32_t)a.ldx + cof;
+        vw = (uint32_t)(wv * 8 + grow) * (uint32_t)a.ldw + cof;
+        // its chunks of a half: half * 4 + h and two further on; their positions differ by xor
+        const int r = l & 31, pos = ((l >> 5) ^ swap_of(r)) << 4;
+        ox = (wm * (BM / WM) + r) * kStep + pos;
+        ow = (BM + wn * (BN / WN) + r) * kStep + pos;
+    };
+    int64_t atx = 0, atw = 0;      // the unit's first rows, and the step in them
+    int jf = uniform(blockIdx.x >> 3), fs = 0, fs1 = 0;   // the next step to bring: unit, step, the unit's end
+    auto aim = [&]() GDN2_INLINE {
+        if (jf >= count) return;
+        const Unit q = unit_of(jf);
+        fs = q.s0;
+        fs1 = q.s1;
+        atx = q.m0 * a.ldx + (int64_t)fs * kStep;
+        atw = q.n0 * a.ldw + (int64_t)fs * kStep;
+    };
+    auto fetch = [&](char *buf) GDN2_INLINE {
+        if (jf >= count) return;
+        const bool in = fs * kStep + cof < (int)a.kbytes;
+        const auto bx = buffer_at(a.x, atx, a.M * a.ldx), bw = buffer_at(a.w, atw, a.N * a.ldw);
+        auto bring = [&](__amdgpu_buffer_rsrc_t from, uint32_t v, char *to) GDN2_INLINE {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16,
+                                                     (int)(in ? v : kBeyond), 0, 0, 0);
+        };
+#pragma unroll
+        for (int i = 0; i < RX; ++i) bring(bx, vx + i * gx, buf + (i * NW + wv) * 1024);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) bring(bw, vw + i * gw, buf + BM * kStep + (i * NW + wv) * 1024);
+        atx += kStep;
+        atw += kStep;
+        if (++fs == fs1) {
+            jf += stride;
+            aim();
+        }
+    };
+
+    // A step's products in phases: half of its bytes, two of the wave's blocks of w. The
+    // operands of the next phase are read while one is multiplied.
+    constexpr int NP = NB / 2, PH = 2 * NP;
+    u4 fw[2][2][2], fx[2][MB][2];   // [phase or half % 2][block][chunk]
+    auto read = [&](const char *buf, auto phase) GDN2_INLINE {
+        constexpr int P = decltype(phase)::value, H = P / NP, J = P % NP * 2;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                fw[P & 1][j][c] = *reinterpret_cast<const u4 *>(buf + (J + j) * 32 * kStep + (ow ^ (H * 64 + c * 32)));
+            if constexpr (J == 0)
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+                    fx[H][i][c] = *reinterpret_cast<const u4 *>(buf + i * 32 * kStep + (ox ^ (H * 64 + c * 32)));
+        }
+    };
+    f16v acc[NB][MB];
+    auto multiply = [&](auto phase) GDN2_INLINE {
+        constexpr int P = decltype(phase)::value, H = P / NP, J = P % NP * 2;
+        __builtin_amdgcn_sched_barrier(0);   // the next phase's operands first, ...
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[J + j][i] = mma32<T>(fw[P & 1][j], fx[H][i], acc[J + j][i]);
+        __builtin_amdgcn_sched_barrier(0);   // ... but not those of the one after
+    };
+    using p0 = std::integral_constant<int, 0>;
+    using last = std::integral_constant<int, PH - 1>;
+
+    int jc = jf, odd = 0;   // the unit in hand; which buffer its step is in
+    if (jc >= count) return;
+    aim();
+    place();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) fetch(lds + i * BUF);
+    landed();
+    __syncthreads();
+    for (; jc < count; jc += stride) {
+        const Unit q = unit_of(jc);
+        place();
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int c = 0; c < 16; ++c) acc[j][i][c] = 0.f;
+        read(lds + odd * BUF, p0{});
+        for (int s = q.s0; s < q.s1; ++s) {
+            const char *cur = lds + odd * BUF;
+            if constexpr (NP == 2) {
+                read(cur, std::integral_constant<int, 1>{});
+                multiply(p0{});
+                read(cur, std::integral_constant<int, 2>{});
+                multiply(std::integral_constant<int, 1>{});
+                read(cur, last{});
+                multiply(std::integral_constant<int, 2>{});
+            } else {
+                read(cur, last{});
+                multiply(p0{});
+            }
+            // (not to be moved behind the barrier and the branches that follow)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int i = 0; i < MB; ++i) asm volatile("" : "+v"(acc[j][i]));
+            landed();
+            __syncthreads();
+            fetch(lds + odd * BUF);
+            odd ^= 1;
+            // (behind a tile's last step: read once more below)
+            read(lds + odd * BUF, p0{});
+            multiply(last{});
+        }
+
+        // The epilogue, block by block. The arguments come from memory anew: kept in
+        // registers they would be in the way above.
+        const GemmArgs e = arguments();
+        const int mw = q.m0 + wm * (BM / WM), nw = q.n0 + wn * (BN / WN);
+        if (mw >= e.M || nw >= e.N) continue;
+        char *mine = lds + 2 * BUF + wv * 4096;
+        if (e.splits > 1) {
+            finish_blocks<T, float, true, MB, NB>(e, (int64_t)q.part * e.M * e.N, mw, nw, lane, mine, acc);
+        } else if (e.out_bf16) {
+            finish_blocks<T, uint16_t, false, MB, NB>(e, 0, mw, nw, lane, mine, acc);
+        } else {
+            finish_blocks<T, float, false, MB, NB>(e, 0, mw, nw, lane, mine, acc);
+        }
+    }
+}
+
+// The same with rows that do not begin at whole chunks or end with them: chunks go
+// through registers, tiles of 128 x 128, 16 x 16 sums an instruction.
+template <Elt T> __global__ __launch_bounds__(256) void gemm_odd_kernel(GemmArgs a, int tm, int tn)
+{
+    constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
+    constexpr int NW = WM * WN, MB = BM / WM / 16, NB = BN / WN / 16;
+    constexpr int RX = BM / 8 / NW, RW = BN / 8 / NW;
+    constexpr int BUF = (BM + BN) * kStep;
     __shared__ __attribute__((aligned(1024))) char lds[2 * BUF + 16 * (BM / 2)];   // (the sums' rows are a little longer)
     const int lane = threadIdx.x & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
-    // neighbouring tiles to one XCD (workgroups go round the eight of them)
-    int tile;
-    {
-        const int all = tm * tn, id = blockIdx.x, xcd = id & 7, q = all >> 3, rest = all & 7;
-        tile = xcd * q + min(xcd, rest) + (id >> 3);
-    }
-    // tiles in bands of four of x's
-    const int band = tile / (4 * tn), inb = tile % (4 * tn), bm = min(4, tm - band * 4);
+    const int band = blockIdx.x / (4 * tn), inb = blockIdx.x % (4 * tn), bm = min(4, tm - band * 4);
     const int64_t m0 = (int64_t)(band * 4 + inb % bm) * BM, n0 = (int64_t)(inb / bm) * BN;
-
-    // what this lane brings: row lane / 8 of a group, and the chunk that belongs at position lane % 8
-    const int grow = lane >> 3;
-    const int cx = ((lane & 7) ^ swap_x((wv & 1) * 8 + grow)) * 16, cw = ((lane & 7) ^ swap_w((wv & 3) * 8 + grow)) * 16;
+    const int grow = lane >> 3, cof = ((lane & 7) ^ swap_of((wv & 1) * 8 + grow)) * 16;
     const char *px[RX], *pw[RW];
 #pragma unroll
-    for (int i = 0; i < RX; ++i) px[i] = (const char *)a.x + min(m0 + (i * NW + wv) * 8 + grow, a.M - 1) * a.ldx + cx;
+    for (int i = 0; i < RX; ++i) px[i] = (const char *)a.x + min(m0 + (i * NW + wv) * 8 + grow, a.M - 1) * a.ldx;
 #pragma unroll
-    for (int i = 0; i < RW; ++i) pw[i] = (const char *)a.w + min(n0 + (i * NW + wv) * 8 + grow, a.N - 1) * a.ldw + cw;
+    for (int i = 0; i < RW; ++i) pw[i] = (const char *)a.w + min(n0 + (i * NW + wv) * 8 + grow, a.N - 1) * a.ldw;
     const int steps = (int)((a.kbytes + kStep - 1) / kStep);
-    const int s0 = (int)((int64_t)steps * blockIdx.y / a.splits), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / a.splits);
 
-    u4 staged[ODD ? RX + RW : 1];
-    auto bring = [&](const char *p, char *to) {
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)p,
-                                         (__attribute__((address_space(3))) void *)to, 16, 0, 0);
-    };
-    auto fetch = [&](int s, char *buf) {
-        const int64_t k = (int64_t)s * kStep;
-        if constexpr (ODD) {
+    u4 staged[RX + RW];
+    auto fetch = [&](int s) {
+        const int64_t k = (int64_t)s * kStep + cof;
 #pragma unroll
-            for (int i = 0; i < RX; ++i) staged[i] = load_chunk<T, true>(px[i] - cx, k + cx, a.kbytes);
+        for (int i = 0; i < RX; ++i) staged[i] = load_chunk<T, true>(px[i], k, a.kbytes);
 #pragma unroll
-            for (int i = 0; i < RW; ++i) staged[RX + i] = load_chunk<T, true>(pw[i] - cw, k + cw, a.kbytes);
-        } else if (k + kStep <= a.kbytes) {
-#pragma unroll
-            for (int i = 0; i < RX; ++i) bring(px[i] + k, buf + (i * NW + wv) * 1024);
-#pragma unroll
-            for (int i = 0; i < RW; ++i) bring(pw[i] + k, buf + BM * kStep + (i * NW + wv) * 1024);
-        } else {
-            const char *zeros = (const char *)kZeros;
-#pragma unroll
-            for (int i = 0; i < RX; ++i) bring(k + cx < a.kbytes ? px[i] + k : zeros, buf + (i * NW + wv) * 1024);
-#pragma unroll
-            for (int i = 0; i < RW; ++i)
-                bring(k + cw < a.kbytes ? pw[i] + k : zeros, buf + BM * kStep + (i * NW + wv) * 1024);
-        }
+        for (int i = 0; i < RW; ++i) staged[RX + i] = load_chunk<T, true>(pw[i], k, a.kbytes);
     };
     auto settle = [&](char *buf) {
-        if constexpr (ODD) {
 #pragma unroll
-            for (int i = 0; i < RX; ++i) *reinterpret_cast<u4 *>(buf + (i * NW + wv) * 1024 + lane * 16) = staged[i];
+        for (int i = 0; i < RX; ++i) *reinterpret_cast<u4 *>(buf + (i * NW + wv) * 1024 + lane * 16) = staged[i];
 #pragma unroll
-            for (int i = 0; i < RW; ++i)
-                *reinterpret_cast<u4 *>(buf + BM * kStep + (i * NW + wv) * 1024 + lane * 16) = staged[RX + i];
-        }
+        for (int i = 0; i < RW; ++i)
+            *reinterpret_cast<u4 *>(buf + BM * kStep + (i * NW + wv) * 1024 + lane * 16) = staged[RX + i];
     };
-
     f4 acc[NB][MB];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
@@ -348,27 +672,19 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(GemmArgs a, int
         for (int i = 0; i < MB; ++i) acc[j][i] = f4zero();
     const int wm = wv % WM, wn = wv / WM;
     // chunk g of this lane's row of a block; chunk g + 4 is at the same place ^ 64
-    const int wrow = 8 * (r >> 2) + (r & 3);
-    const int ox = (wm * (BM / WM) + r) * kStep + ((g ^ swap_x(r)) << 4);
-    int ow[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        ow[j] = (BM + wn * (BN / WN) + wrow + 4 * j) * kStep + ((g ^ swap_w(wrow + 4 * j)) << 4);
-
-    if (s0 < s1) {
-        fetch(s0, lds);
-        settle(lds);
-    }
-    for (int s = s0; s < s1; ++s) {
-        char *cur = lds + ((s - s0) & 1) * BUF, *next = lds + ((s - s0 + 1) & 1) * BUF;
-        __syncthreads();   // (waits for this wave's loads into cur, and for every wave to have left next)
-        if (s + 1 < s1) fetch(s + 1, next);
+    const int pos = (g ^ swap_of(r)) << 4;
+    const int ox = (wm * (BM / WM) + r) * kStep + pos, ow = (BM + wn * (BN / WN) + r) * kStep + pos;
+    fetch(0);
+    settle(lds);
+    for (int s = 0; s < steps; ++s) {
+        char *cur = lds + (s & 1) * BUF, *next = lds + ((s + 1) & 1) * BUF;
+        __syncthreads();
+        if (s + 1 < steps) fetch(s + 1);
         u4 fw[NB][2];
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                fw[j][c] = *reinterpret_cast<const u4 *>(cur + (j >> 1) * 32 * kStep + (ow[j & 1] ^ (64 * c)));
+            for (int c = 0; c < 2; ++c) fw[j][c] = *reinterpret_cast<const u4 *>(cur + j * 16 * kStep + (ow ^ (64 * c)));
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             u4 fx[2];
@@ -377,11 +693,9 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(GemmArgs a, int
 #pragma unroll
             for (int j = 0; j < NB; ++j) acc[j][i] = Mm<T>::mma(fw[j], fx, acc[j][i]);
         }
-        if (s + 1 < s1) settle(next);
+        if (s + 1 < steps) settle(next);
     }
-
-    // The sums go through LDS, so that lanes take whole lines of y (and of the
-    // residual), eight elements each, in a short loop. kRows of each wave's rows a round.
+    // the sums through LDS, half of each wave's rows a round, eight neighbours a lane
     constexpr int PITCH = BN + 4, kRows = 16 * (MB / 2), TPR = BN / 8;
     static_assert(WM * kRows * PITCH * 4 <= (int)sizeof(lds), "the sums of a round");
     float *sums = reinterpret_cast<float *>(lds);
@@ -392,8 +706,8 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(GemmArgs a, int
         for (int i = 0; i < MB / 2; ++i)
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-                *reinterpret_cast<f4 *>(&sums[(wm * kRows + i * 16 + r) * PITCH + wn * (BN / WN) + (j >> 1) * 32 + (j & 1) * 4 +
-                                              g * 8]) = acc[j][q * (MB / 2) + i];
+                *reinterpret_cast<f4 *>(&sums[(wm * kRows + i * 16 + r) * PITCH + wn * (BN / WN) + j * 16 + g * 4]) =
+                    acc[j][q * (MB / 2) + i];
         __syncthreads();
         const int col = threadIdx.x % TPR * 8;
         const int64_t n = n0 + col;
@@ -402,15 +716,16 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(GemmArgs a, int
             for (int row = threadIdx.x / TPR; row < WM * kRows; row += NW * 64 / TPR) {
                 const int64_t m = m0 + row / kRows * (BM / WM) + q * kRows + row % kRows;
                 if (m >= a.M) continue;
+                Finish8 fin;
+                fin.load(a, m, n, cnt);
                 float v[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const f4 x = *reinterpret_cast<const f4 *>(&sums[row * PITCH + col + h * 4]);
+                for (int e = 0; e < 2; ++e) {
+                    const f4 x = *reinterpret_cast<const f4 *>(&sums[row * PITCH + col + e * 4]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[h * 4 + c] = x[c];
+                    for (int c = 0; c < 4; ++c) v[e * 4 + c] = x[c];
                 }
-                if (a.splits > 1) put8(a.partial + ((int64_t)blockIdx.y * a.M + m) * a.N + n, cnt, v);
-                else finish8(a, m, n, cnt, v);
+                fin.store(a, m, n, cnt, v);
             }
         }
     }
@@ -423,14 +738,16 @@ static __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs a)
     if (e >= a.M * runs) return;
     const int64_t m = e / runs, n = e % runs * 8;
     const int cnt = (int)min((int64_t)8, a.N - n);
+    Finish8 fin;
+    fin.load(a, m, n, cnt);
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < a.splits; ++s) {
         float x[8];
-        get8(a.partial + ((int64_t)s * a.M + m) * a.N + n, cnt, x);
+        get8(a.partial + ((int64_t)s * a.M + m) * a.ldp + n, cnt, x);
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[c] += x[c];
     }
-    finish8(a, m, n, cnt, v);
+    fin.store(a, m, n, cnt, v);
 }
 
 // ---- launch -------------------------------------------------------------------------
@@ -445,12 +762,19 @@ template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a
         hipLaunchKernelGGL((gemm_split_kernel<T, MB, NB, ODD>), dim3((unsigned)gx, (unsigned)gy), dim3(kWaves * 64), 0, st, a);
         return hipGetLastError();
     };
-    auto tiled = [&](auto bm, auto bn, auto wm, auto wn) {
-        constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value;
-        const int64_t tm = tiles(a.M, BM), tn = tiles(a.N, BN);
+    auto tiled = [&](auto odd, auto b, auto wm, auto wn) {
+        constexpr int B = decltype(b)::value, WM = decltype(wm)::value, WN = decltype(wn)::value;
+        const int64_t tm = tiles(a.M, B), tn = tiles(a.N, B);
         if (tm * tn > 0x7fffffLL) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, WM, WN, ODD>), dim3((unsigned)(tm * tn), a.splits),
-                           dim3(WM * WN * 64), 0, st, a, (int)tm, (int)tn);
+        if constexpr (decltype(odd)::value) {
+            static_assert(B == 128, "its tiles");
+            hipLaunchKernelGGL(gemm_odd_kernel<T>, dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, (int)tm, (int)tn);
+        } else {
+            // as many workgroups as there is room for (one or two a compute unit), a multiple of the XCDs'
+            const int64_t grid = std::min<int64_t>((tm * tn * a.splits + 7) / 8 * 8, B == 256 ? 256 : 512);
+            hipLaunchKernelGGL((gemm_tile_kernel<T, B, B, WM, WN>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, st, a,
+                               (int)tm, (int)tn);
+        }
         return hipGetLastError();
     };
     using i1 = std::integral_constant<int, 1>;
@@ -463,20 +787,24 @@ template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a
         if (a.M <= 64) return split(i4{}, i1{});
         if (tiles(a.M, 64) * tiles(a.N, 64) <= 512) return split(i4{}, i4{});
     }
-    if constexpr (!ODD) {
-        using i256 = std::integral_constant<int, 256>;
-        if (tiles(a.M, 256) * tiles(a.N, 256) * a.splits >= 192) return tiled(i256{}, i256{}, i4{}, i2{});
-    }
-    return tiled(i128{}, i128{}, i2{}, i2{});
+    if (ODD || a.N % 8 != 0) return tiled(std::true_type{}, i128{}, i2{}, i2{});
+    using i256 = std::integral_constant<int, 256>;
+    if (tiles(a.M, 256) * tiles(a.N, 256) * a.splits >= 192) return tiled(std::false_type{}, i256{}, i4{}, i2{});
+    return tiled(std::false_type{}, i128{}, i2{}, i2{});
 }
 
 template <Elt T> static hipError_t launch_gemm_type(const GemmArgs &a, hipStream_t st)
 {
-    const bool odd = a.ldx % 16 || a.ldw % 16 || a.kbytes % 16;
-    const hipError_t err = odd ? launch_gemm_forms<T, true>(a, st) : launch_gemm_forms<T, false>(a, st);
-    if (err != hipSuccess || a.splits == 1) return err;
+    if (a.splits == 1) {
+        const bool odd = a.ldx % 16 || a.ldw % 16 || a.kbytes % 16;
+        return odd ? launch_gemm_forms<T, true>(a, st) : launch_gemm_forms<T, false>(a, st);
+    }
     const int64_t blocks = (a.M * ((a.N + 7) / 8) + 255) / 256;
-    if (blocks > 0xffffffLL) return hipErrorInvalidConfiguration;
+    if (blocks > 0xffffffLL || a.ldp % 8 || a.ldp < a.N) return hipErrorInvalidConfiguration;
+    GemmArgs part = a;
+    part.N = a.ldp;
+    const hipError_t err = launch_gemm_forms<T, false>(part, st);
+    if (err != hipSuccess) return err;
     hipLaunchKernelGGL(gemm_join_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a);
     return hipGetLastError();
 }

@@ -533,7 +533,8 @@ int gdn2_layer_norm_bwd(const void *dy, const void *h, const float *weight, cons
  * GDN2_BF16. No output, nor the workspace, may overlap an input or another
  * output. workspace: gdn2_linear_bwd_workspace_bytes(...) of device memory.
  *
- * rows >= 0; 1 <= in_features, out_features <= GDN2_LINEAR_MAX_FEATURES.
+ * rows >= 0 (the gradient: up to GDN2_LINEAR_BWD_MAX_ROWS);
+ * 1 <= in_features, out_features <= GDN2_LINEAR_MAX_FEATURES.
  * GDN2_ERR_UNSUPPORTED for products of two of the three sizes of about 2^37
  * and more. Pointers are 16-byte aligned; the sizes may be any number
  * (in_features in whole 16 bytes and out_features in whole eights are faster).
@@ -545,6 +546,7 @@ typedef enum {
     GDN2_ACT_GELU_TANH = 3
 } gdn2_activation;
 #define GDN2_LINEAR_MAX_FEATURES (1 << 20)
+#define GDN2_LINEAR_BWD_MAX_ROWS (1 << 22)
 int gdn2_linear_fwd(const void *x, const void *weight, const float *bias, const void *residual, const float *x_scale,
                     const float *weight_scale, void *y, void *preact, int64_t rows, int in_features, int out_features,
                     int activation, int in_dtype, int out_dtype);
