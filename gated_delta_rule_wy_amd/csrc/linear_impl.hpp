@@ -319,6 +319,7 @@ static __device__ __forceinline__ GemmArgs arguments()
 // whole in the vector operand, which the bounds are checked against; kBeyond is
 // outside always.
 constexpr uint32_t kBeyond = 0xFFFFFF80u;   // (and 16 bytes on)
+constexpr int kOnce = 2;   // cache policy: not to be kept (y would push x's and w's lines out of the L2)
 static __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void *base, int64_t at, int64_t end)
 {
     const uint32_t left = (end - at) >> 32 ? 0xFFFFFF00u : (uint32_t)(end - at);
@@ -410,12 +411,12 @@ static __device__ __forceinline__ void finish_blocks(const GemmArgs &e, int64_t 
                 const int o = offset(j, i, t, sizeof(type));
                 if constexpr (sizeof(type) == 2) {
                     const u4 x = {bf16x2(v[t][0], v[t][1]), bf16x2(v[t][2], v[t][3]), bf16x2(v[t][4], v[t][5]), bf16x2(v[t][6], v[t][7])};
-                    __builtin_amdgcn_raw_buffer_store_b128(x, p, o, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(x, p, o, 0, kOnce);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const f4 x = {v[t][k * 4], v[t][k * 4 + 1], v[t][k * 4 + 2], v[t][k * 4 + 3]};
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), p, o + k * 16, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), p, o + k * 16, 0, PART ? 0 : kOnce);
                     }
                 }
             }
