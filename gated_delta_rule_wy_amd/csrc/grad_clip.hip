@@ -96,18 +96,18 @@ __global__ __launch_bounds__(kThreads) void clip_norm_kernel(ClipBatch b, double
     if (threadIdx.x == 0) partial[blockIdx.x] = (further ? partial[blockIdx.x] : 0.) + s;
 }
 
-static __device__ __forceinline__ float norm_of(const double *partial, int parts, double *red)
+static __device__ __forceinline__ double norm_of(const double *partial, int parts, double *red)
 {
     double s = 0.;
     for (int i = threadIdx.x; i < parts; i += kThreads) s += partial[i];
-    return (float)sqrt(block_sum(s, red));
+    return sqrt(block_sum(s, red));
 }
 
 __global__ __launch_bounds__(kThreads) void clip_finish_kernel(const double *partial, int parts, float *norm)
 {
     __shared__ double red[kThreads / 64];
-    const float x = norm_of(partial, parts, red);
-    if (threadIdx.x == 0) *norm = x;
+    const double x = norm_of(partial, parts, red);
+    if (threadIdx.x == 0) *norm = (float)x;
 }
 
 static __device__ __forceinline__ void store_some(uint16_t *p, const float (&x)[8], int n)
@@ -144,9 +144,10 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipBatch b, const
                                                               const float *norm_in, float *norm_out, float max_norm)
 {
     __shared__ double red[kThreads / 64];
-    const float norm = norm_in ? *norm_in : norm_of(partial, parts, red);
-    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    const double q = (double)max_norm / ((double)norm + 1e-6);
+    // (a norm beyond the largest float still scales by what it is)
+    const double norm = norm_in ? (double)*norm_in : norm_of(partial, parts, red);
+    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+    const double q = (double)max_norm / (norm + 1e-6);
     const float c = q >= 1. ? 1.f : (float)q;   // (NaN stays)
     for (int i = blockIdx.x; i < b.pieces; i += gridDim.x) {
         const int p = b.pieces - 1 - i, t = tensor_of(b, p);

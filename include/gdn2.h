@@ -520,7 +520,10 @@ int gdn2_layer_norm_bwd(const void *dy, const void *h, const float *weight, cons
  * act: none, sigmoid, silu z sigmoid(z), or gelu in its tanh form
  *   0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))).
  * e4m3 is the 8-bit float with 4 exponent and 3 mantissa bits, no infinities
- * and largest value 448. Products are exact and sums fp32, in a fixed order.
+ * and largest value 448. Products are exact and sums fp32, in a fixed order; of
+ * e4m3 products, aligned eights along k are first added with 13 bits below the
+ * largest of them (the matrix instruction's way: an error of up to 2^-13 of it
+ * for each of the others).
  * Otherwise no output overlaps an input or another output (GDN2_ERR_INVALID
  * where two pointers are one; partial overlaps are not checked).
  *
@@ -601,8 +604,9 @@ int gdn2_rms_norm_bwd(const void *dy, const void *h, const float *weight, const 
  * is to be scaled); otherwise no out[i] may overlap any grads[j] or out[j]
  * (GDN2_ERR_INVALID; checked over their whole length). Tensors lie at any
  * multiple of their element's size. Squares and their sums are fp64, in a fixed
- * order. An infinite norm makes finite gradients 0 and infinite ones NaN; a NaN
- * one makes all of them NaN. 0 <= max_norm, finite.
+ * order; a norm beyond the largest float is written as infinity, and scales by what
+ * it is. Infinite gradients make finite ones 0 and themselves NaN; a NaN makes all
+ * of them NaN. 0 <= max_norm, finite.
  */
 size_t gdn2_clip_grads_workspace_bytes(void);
 int gdn2_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int count, float *norm,
