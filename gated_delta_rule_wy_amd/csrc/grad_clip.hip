@@ -110,33 +110,44 @@ __global__ __launch_bounds__(kThreads) void clip_finish_kernel(const double *par
     if (threadIdx.x == 0) *norm = (float)x;
 }
 
-static __device__ __forceinline__ void store_some(uint16_t *p, const float (&x)[8], int n)
-{
-    for (int i = 0; i < n; ++i) store1(p + i, x[i]);
-}
-static __device__ __forceinline__ void store_some(float *p, const float (&x)[8], int n)
-{
-    for (int i = 0; i < n; ++i) store1(p + i, x[i]);
-}
-
+// n elements of p (kPiece at most) to o, times c. A lane takes eight neighbours at a time, or four where one
+// side is fp32, so that a wave's loads and stores are each in one piece (235 M bf16 to fp32: OLDUS us
+// with eight, NEWUS with four).
 template <typename In, typename Out>
 static __device__ __forceinline__ void piece_scale(const In *p, Out *o, int64_t n, float c)
 {
-    Pack8<In> x[kRounds];
+    constexpr int V = sizeof(In) + sizeof(Out) > 4 ? 4 : 8, R = 8;   // rounds whose loads are under way at once
+    typedef uint32_t vin __attribute__((ext_vector_type(V * sizeof(In) / 4)));
+    typedef uint32_t vout __attribute__((ext_vector_type(V * sizeof(Out) / 4)));
+    typedef vin vin_any __attribute__((aligned(sizeof(In))));
+    typedef vout vout_any __attribute__((aligned(sizeof(Out))));
+    auto get = [](const vin &x, int i) {
+        if constexpr (sizeof(In) == 4) return __uint_as_float(x[i]);
+        else return __uint_as_float((i & 1) ? (x[i >> 1] & 0xFFFF0000u) : (x[i >> 1] << 16));
+    };
+#pragma unroll 1
+    for (int first = 0; first < kPiece; first += R * kThreads * V) {
+        vin x[R];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const int at = (r * kThreads + (int)threadIdx.x) * 8;
-        if (at + 8 <= n) x[r].template load<false, false>(p + at);
-        else x[r].load_some(p + at, (int)min(n, (int64_t)kPiece) - at);
-    }
+        for (int r = 0; r < R; ++r) {
+            const int at = first + (r * kThreads + (int)threadIdx.x) * V;
+            if (at + V <= n) x[r] = __builtin_nontemporal_load(reinterpret_cast<const vin_any *>(p + at));
+        }
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const int at = (r * kThreads + (int)threadIdx.x) * 8;
-        float y[8];
+        for (int r = 0; r < R; ++r) {
+            const int at = first + (r * kThreads + (int)threadIdx.x) * V;
+            if (at + V <= n) {
+                vout y;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[r].get(i) * c;
-        if (at + 8 <= n) store8<false>(o + at, y);
-        else if (at < n) store_some(o + at, y, (int)(n - at));
+                for (int i = 0; i < V; ++i) {
+                    if constexpr (sizeof(Out) == 4) y[i] = __float_as_uint(get(x[r], i) * c);
+                    else if (i % 2 == 0) y[i / 2] = bf16x2(get(x[r], i) * c, get(x[r], i + 1) * c);
+                }
+                __builtin_nontemporal_store(y, reinterpret_cast<vout_any *>(o + at));
+            } else {
+                for (int i = at; i < n && i < at + V; ++i) store1(o + i, in2f<In>(p[i]) * c);
+            }
+        }
     }
 }
 

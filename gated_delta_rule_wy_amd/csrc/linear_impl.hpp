@@ -64,30 +64,38 @@ template <> struct Mm<Elt::kE4m3> {
     }
 };
 
-// Chunk at byte `at` of a row of `bytes`, zeros behind its end. ODD: rows begin
-// at any element, and a row's last chunk may be a part of one.
-template <Elt T, bool ODD> static __device__ __forceinline__ u4 load_chunk(const char *row, int64_t at, int64_t bytes)
+// Chunk at byte `at` of a row of `bytes` that begins at any element and may end
+// with a part of one; zeros behind its end.
+template <Elt T> static __device__ __forceinline__ u4 load_chunk(const char *row, int64_t at, int64_t bytes)
 {
     u4 r = {0u, 0u, 0u, 0u};
-    if constexpr (!ODD) {
-        if (at < bytes) r = *reinterpret_cast<const u4 *>(row + at);
+    if (at + 16 <= bytes) {
+        r = *reinterpret_cast<const u4_byte *>(row + at);
     } else {
-        if (at + 16 <= bytes) {
-            r = *reinterpret_cast<const u4_byte *>(row + at);
-        } else {
-            constexpr int S = Mm<T>::kSize;
+        constexpr int S = Mm<T>::kSize;
 #pragma unroll
-            for (int i = 0; i < 16; i += S)
-                if (at + i < bytes) {
-                    uint32_t v;
-                    if constexpr (S == 4) v = *reinterpret_cast<const uint32_t *>(row + at + i);
-                    else if constexpr (S == 2) v = *reinterpret_cast<const uint16_t *>(row + at + i);
-                    else v = *reinterpret_cast<const uint8_t *>(row + at + i);
-                    r[i / 4] |= v << (8 * (i % 4));
-                }
-        }
+        for (int i = 0; i < 16; i += S)
+            if (at + i < bytes) {
+                uint32_t v;
+                if constexpr (S == 4) v = *reinterpret_cast<const uint32_t *>(row + at + i);
+                else if constexpr (S == 2) v = *reinterpret_cast<const uint16_t *>(row + at + i);
+                else v = *reinterpret_cast<const uint8_t *>(row + at + i);
+                r[i / 4] |= v << (8 * (i % 4));
+            }
     }
     return r;
+}
+
+// A buffer descriptor from `at` bytes into `base` to its end at `end` bytes: what is
+// read beyond arrives as zeros, what is written there is dropped. Offsets are
+// whole in the vector operand, which the bounds are checked against; kBeyond is
+// outside always.
+constexpr uint32_t kBeyond = 0xFFFFFF80u;   // (and 16 bytes on)
+constexpr int kOnce = 2;   // cache policy: not to be kept (y would push x's and w's lines out of the L2)
+static __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void *base, int64_t at, int64_t end)
+{
+    const uint32_t left = (end - at) >> 32 ? 0xFFFFFF00u : (uint32_t)(end - at);
+    return __builtin_amdgcn_make_buffer_rsrc((char *)const_cast<void *>(base) + at, (short)0, (int)left, 0x00020000);
 }
 
 // ---- the epilogue ----------------------------------------------------------------
@@ -192,13 +200,14 @@ struct Finish8 {
 
 // ---- few tiles: every wave a part of the contraction -----------------------------
 //
-// A workgroup of W waves owns 16 MB rows of x and 16 NB of w. Wave i takes the
-// steps i, i + W, ... straight from memory into the instructions' operands
-// (nothing is used twice that could be shared through LDS), and the waves' sums are
-// added through LDS in wave order.
+// A workgroup of eight waves owns 16 MB rows of x and 16 NB of w. Wave i takes the
+// steps i, i + 8, ... straight from memory into the instructions' operands
+// (nothing is used twice that could be shared through LDS), D - 1 of them on their way while
+// one is multiplied, and the waves' sums are added through LDS in wave order.
 constexpr int kWaves = 8;
 
-template <Elt T, int MB, int NB, bool ODD> __global__ __launch_bounds__(kWaves * 64) void gemm_split_kernel(GemmArgs a)
+template <Elt T, int MB, int NB, int D, bool ODD>
+__global__ __launch_bounds__(kWaves * 64) void gemm_split_kernel(GemmArgs a)
 {
     constexpr int PITCH = NB * 16 + 4;                   // floats a row of the sums (16-byte aligned, banks apart)
     constexpr int ROUNDS = MB * NB > 4 ? 2 : 1, MR = MB / ROUNDS;   // blocks of rows a round through LDS
@@ -206,34 +215,52 @@ template <Elt T, int MB, int NB, bool ODD> __global__ __launch_bounds__(kWaves *
     __shared__ __attribute__((aligned(16))) float sums[kWaves][MR * 16 * PITCH];
     const int lane = threadIdx.x & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
     const int64_t m0 = (int64_t)blockIdx.y * (MB * 16), n0 = (int64_t)blockIdx.x * (NB * 16);
-    const char *px[MB], *pw[NB];
+    const auto bx = buffer_at(a.x, m0 * a.ldx, a.M * a.ldx), bw = buffer_at(a.w, n0 * a.ldw, a.N * a.ldw);
+    struct Frags { u4 x[MB][2], w[NB][2]; } f[D];
+    auto load = [&](Frags &q, int s) GDN2_INLINE {
+        const int at = s * kStep + g * 32;
 #pragma unroll
-    for (int i = 0; i < MB; ++i) px[i] = (const char *)a.x + min(m0 + i * 16 + r, a.M - 1) * a.ldx;
+        for (int c = 0; c < 2; ++c) {
+            if constexpr (ODD) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) pw[i] = (const char *)a.w + min(n0 + i * 16 + r, a.N - 1) * a.ldw;
+                for (int j = 0; j < NB; ++j)
+                    q.w[j][c] = load_chunk<T>((const char *)a.w + min(n0 + j * 16 + r, a.N - 1) * a.ldw, at + c * 16, a.kbytes);
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+                    q.x[i][c] = load_chunk<T>((const char *)a.x + min(m0 + i * 16 + r, a.M - 1) * a.ldx, at + c * 16, a.kbytes);
+            } else {
+                const bool in = at + c * 16 < (int)a.kbytes;
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    q.w[j][c] = __builtin_amdgcn_raw_buffer_load_b128(
+                        bw, (int)(in ? (uint32_t)(j * 16 + r) * (uint32_t)a.ldw + (uint32_t)(at + c * 16) : kBeyond), 0, 0);
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+                    q.x[i][c] = __builtin_amdgcn_raw_buffer_load_b128(
+                        bx, (int)(in ? (uint32_t)(i * 16 + r) * (uint32_t)a.ldx + (uint32_t)(at + c * 16) : kBeyond), 0, 0);
+            }
+        }
+    };
     f4 acc[NB][MB];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int i = 0; i < MB; ++i) acc[j][i] = f4zero();
-    const int steps = (int)((a.kbytes + kStep - 1) / kStep);
-#pragma unroll 2
-    for (int s = wv; s < steps; s += kWaves) {
-        const int64_t k = (int64_t)s * kStep + g * 32;
-        u4 fx[MB][2], fw[NB][2];
+    const int steps = (int)((a.kbytes + kStep - 1) / kStep), mine = (steps - wv + kWaves - 1) / kWaves;
+    auto step = [&](int i) GDN2_INLINE { return wv + i * kWaves; };
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
+    for (int d = 0; d < D - 1; ++d)
+        if (d < mine) load(f[d], step(d));
+    for (int i = 0; i < mine; i += D)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) fw[j][c] = load_chunk<T, ODD>(pw[j], k + c * 16, a.kbytes);
+        for (int d = 0; d < D; ++d) {
+            if (i + d >= mine) break;
+            if (i + d + D - 1 < mine) load(f[(d + D - 1) % D], step(i + d + D - 1));
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+            for (int j = 0; j < NB; ++j)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) fx[i][c] = load_chunk<T, ODD>(px[i], k + c * 16, a.kbytes);
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int i = 0; i < MB; ++i) acc[j][i] = Mm<T>::mma(fw[j], fx[i], acc[j][i]);
-    }
+                for (int k = 0; k < MB; ++k) acc[j][k] = Mm<T>::mma(f[d].w[j], f[d].x[k], acc[j][k]);
+        }
 #pragma unroll
     for (int q = 0; q < ROUNDS; ++q) {
         if (q) __syncthreads();
@@ -316,18 +343,6 @@ static __device__ __forceinline__ GemmArgs arguments()
     auto p = (const __attribute__((address_space(4))) GemmArgs *)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(p));
     return *(const GemmArgs *)p;
-}
-
-// A buffer descriptor from `at` bytes into `base` to its end at `end` bytes: what is
-// read beyond arrives as zeros, what is written there is dropped. Offsets are
-// whole in the vector operand, which the bounds are checked against; kBeyond is
-// outside always.
-constexpr uint32_t kBeyond = 0xFFFFFF80u;   // (and 16 bytes on)
-constexpr int kOnce = 2;   // cache policy: not to be kept (y would push x's and w's lines out of the L2)
-static __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void *base, int64_t at, int64_t end)
-{
-    const uint32_t left = (end - at) >> 32 ? 0xFFFFFF00u : (uint32_t)(end - at);
-    return __builtin_amdgcn_make_buffer_rsrc((char *)const_cast<void *>(base) + at, (short)0, (int)left, 0x00020000);
 }
 
 // The epilogue of a wave's blocks, from row mw and column nw of y on. Each 32 x 32
@@ -659,9 +674,9 @@ template <Elt T> __global__ __launch_bounds__(256) void gemm_odd_kernel(GemmArgs
     auto fetch = [&](int s) {
         const int64_t k = (int64_t)s * kStep + cof;
 #pragma unroll
-        for (int i = 0; i < RX; ++i) staged[i] = load_chunk<T, true>(px[i], k, a.kbytes);
+        for (int i = 0; i < RX; ++i) staged[i] = load_chunk<T>(px[i], k, a.kbytes);
 #pragma unroll
-        for (int i = 0; i < RW; ++i) staged[RX + i] = load_chunk<T, true>(pw[i], k, a.kbytes);
+        for (int i = 0; i < RW; ++i) staged[RX + i] = load_chunk<T>(pw[i], k, a.kbytes);
     };
     auto settle = [&](char *buf) {
 #pragma unroll
@@ -760,11 +775,11 @@ static __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs a)
 template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a, hipStream_t st)
 {
     auto tiles = [](int64_t rows, int b) { return (rows + b - 1) / b; };
-    auto split = [&](auto mb, auto nb) {
-        constexpr int MB = decltype(mb)::value, NB = decltype(nb)::value;
+    auto split = [&](auto mb, auto nb, auto d) {
+        constexpr int MB = decltype(mb)::value, NB = decltype(nb)::value, D = decltype(d)::value;
         const int64_t gx = tiles(a.N, NB * 16), gy = tiles(a.M, MB * 16);
         if (gy > 65535 || gx * gy > 0x7fffffLL) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL((gemm_split_kernel<T, MB, NB, ODD>), dim3((unsigned)gx, (unsigned)gy), dim3(kWaves * 64), 0, st, a);
+        hipLaunchKernelGGL((gemm_split_kernel<T, MB, NB, D, ODD>), dim3((unsigned)gx, (unsigned)gy), dim3(kWaves * 64), 0, st, a);
         return hipGetLastError();
     };
     auto tiled = [&](auto odd, auto b, auto wm, auto wn) {
@@ -787,10 +802,17 @@ template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a
     using i4 = std::integral_constant<int, 4>;
     using i128 = std::integral_constant<int, 128>;
     if (a.splits == 1) {
-        if (a.M <= 16) return split(i1{}, i1{});
-        if (a.M <= 32) return split(i2{}, i1{});
-        if (a.M <= 64) return split(i4{}, i1{});
-        if (tiles(a.M, 64) * tiles(a.N, 64) <= 512) return split(i4{}, i4{});
+        if (a.M <= 16) return split(i1{}, i1{}, i4{});
+        if (a.M <= 32) return split(i2{}, i1{}, i4{});
+        if (a.M <= 64) return split(i4{}, i1{}, i4{});
+        // the largest blocks that give every compute unit a workgroup
+        if (tiles(a.M, 64) * tiles(a.N, 64) < 256) {
+            if (tiles(a.M, 32) * tiles(a.N, 64) < 256) return split(i2{}, i2{}, i4{});
+            return split(i2{}, i4{}, i2{});
+        }
+        // fp32's matrix instructions take so long that operands from the L2 keep up, and small
+        // blocks leave no compute unit idle at the end
+        if (tiles(a.M, 64) * tiles(a.N, 64) <= 512 || (T == Elt::kF32 && (ODD || a.N % 8 != 0))) return split(i4{}, i4{}, i2{});
     }
     if (ODD || a.N % 8 != 0) return tiled(std::true_type{}, i128{}, i2{}, i2{});
     using i256 = std::integral_constant<int, 256>;
