@@ -252,14 +252,14 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a, hipStream_t st)
 
 int gemm_splits(int64_t M, int64_t N, int64_t kbytes)
 {
-    auto tiles = [&](int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
-    const int64_t steps = (kbytes + 127) / 128, big = tiles(256), small = tiles(128);
+    auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    const int64_t steps = (kbytes + 127) / 128, big = tiles(256, 256), small = tiles(128, 64);
     if (M == 0 || big >= 192) return 1;
-    // one part a compute unit, each of 16 steps (8 of the smaller tiles) at least
-    const int64_t s = std::min((256 + big - 1) / big, steps / 16);
+    // one part a compute unit, each of 16 steps at least
+    int64_t s = std::min((256 + big - 1) / big, steps / 16);
     if (s >= 1 && big * s >= 192) return (int)s;
-    if (M <= 64 || (tiles(64) <= 512 && steps <= 64)) return 1;   // (few tiles: the waves share the contraction)
-    return (int)std::max<int64_t>(1, std::min((256 + small - 1) / small, steps / 8));
+    s = std::min((512 + small - 1) / small, steps / 16);
+    return s >= 2 ? (int)s : 1;
 }
 
 hipError_t launch_gemm(Elt e, const GemmArgs &a, const char *name, hipStream_t st)

@@ -782,42 +782,46 @@ template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a
         hipLaunchKernelGGL((gemm_split_kernel<T, MB, NB, D, ODD>), dim3((unsigned)gx, (unsigned)gy), dim3(kWaves * 64), 0, st, a);
         return hipGetLastError();
     };
-    auto tiled = [&](auto odd, auto b, auto wm, auto wn) {
-        constexpr int B = decltype(b)::value, WM = decltype(wm)::value, WN = decltype(wn)::value;
-        const int64_t tm = tiles(a.M, B), tn = tiles(a.N, B);
+    auto tiled = [&](auto bm, auto bn, auto wm, auto wn) {
+        constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value;
+        const int64_t tm = tiles(a.M, BM), tn = tiles(a.N, BN);
         if (tm * tn > 0x7fffffLL) return hipErrorInvalidConfiguration;
-        if constexpr (decltype(odd)::value) {
-            static_assert(B == 128, "its tiles");
-            hipLaunchKernelGGL(gemm_odd_kernel<T>, dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, (int)tm, (int)tn);
-        } else {
-            // as many workgroups as there is room for (one or two a compute unit), a multiple of the XCDs'
-            const int64_t grid = std::min<int64_t>((tm * tn * a.splits + 7) / 8 * 8, B == 256 ? 256 : 512);
-            hipLaunchKernelGGL((gemm_tile_kernel<T, B, B, WM, WN>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, st, a,
-                               (int)tm, (int)tn);
-        }
+        // as many workgroups as there is room for (one or two a compute unit), a multiple of the XCDs'
+        const int64_t grid = std::min<int64_t>((tm * tn * a.splits + 7) / 8 * 8, WM * WN == 8 ? 256 : 512);
+        hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, WM, WN>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, st, a, (int)tm,
+                           (int)tn);
         return hipGetLastError();
     };
     using i1 = std::integral_constant<int, 1>;
     using i2 = std::integral_constant<int, 2>;
     using i4 = std::integral_constant<int, 4>;
+    using i64 = std::integral_constant<int, 64>;
     using i128 = std::integral_constant<int, 128>;
-    if (a.splits == 1) {
-        if (a.M <= 16) return split(i1{}, i1{}, i4{});
-        if (a.M <= 32) return split(i2{}, i1{}, i4{});
-        if (a.M <= 64) return split(i4{}, i1{}, i4{});
-        // the largest blocks that give every compute unit a workgroup
-        if (tiles(a.M, 64) * tiles(a.N, 64) < 256) {
-            if (tiles(a.M, 32) * tiles(a.N, 64) < 256) return split(i2{}, i2{}, i4{});
-            return split(i2{}, i4{}, i2{});
-        }
-        // fp32's matrix instructions take so long that operands from the L2 keep up, and small
-        // blocks leave no compute unit idle at the end
-        if (tiles(a.M, 64) * tiles(a.N, 64) <= 512 || (T == Elt::kF32 && (ODD || a.N % 8 != 0))) return split(i4{}, i4{}, i2{});
-    }
-    if (ODD || a.N % 8 != 0) return tiled(std::true_type{}, i128{}, i2{}, i2{});
     using i256 = std::integral_constant<int, 256>;
-    if (tiles(a.M, 256) * tiles(a.N, 256) * a.splits >= 192) return tiled(std::false_type{}, i256{}, i4{}, i2{});
-    return tiled(std::false_type{}, i128{}, i2{}, i2{});
+    // fp32's matrix instructions take so long that one step ahead is enough, and that operands
+    // from the L2 keep up with them: small blocks, which leave no compute unit idle at the end, are used far longer
+    // (1024^3: 23 us, 25 with a step ahead, 39 in tiles).
+    constexpr bool kSlow = T == Elt::kF32;
+    using ahead = std::conditional_t<kSlow, i1, i2>;
+    // Rows that LDS can take whole chunks of, and y in whole eights: tiles, the larger ones where they
+    // fill the chip (bf16, K = N = 2048: 1024 rows 18 us in tiles of 128 x 64, 35 in blocks
+    // of the waves that share the contraction; 4096 rows 35 us in 128 x 128, 46 in 128 x 64; 512 rows 16 and 18, 256
+    // rows 16 and 15).
+    const bool whole = !ODD && a.N % 8 == 0;
+    if (whole && tiles(a.M, 256) * tiles(a.N, 256) * a.splits >= 192) return tiled(i256{}, i256{}, i4{}, i2{});
+    if (whole && tiles(a.M, 128) * tiles(a.N, 128) * a.splits >= (kSlow ? 512 : 256)) return tiled(i128{}, i128{}, i2{}, i2{});
+    if (whole && (a.splits > 1 || (!kSlow && tiles(a.M, 128) * tiles(a.N, 64) >= 128))) return tiled(i128{}, i64{}, i4{}, i1{});
+    if (a.M <= 16) return split(i1{}, i1{}, i4{});
+    if (a.M <= 32) return split(i2{}, i1{}, i4{});
+    if (a.M <= 64) return split(i4{}, i1{}, i4{});
+    // the largest blocks that give every compute unit a workgroup (fp32: most of them)
+    if (tiles(a.M, 32) * tiles(a.N, 64) < (kSlow ? 128 : 256)) return split(i2{}, i2{}, i4{});
+    if (tiles(a.M, 64) * tiles(a.N, 64) < (kSlow ? 192 : 256)) return split(i2{}, i4{}, ahead{});
+    if (kSlow || tiles(a.M, 64) * tiles(a.N, 64) <= 512) return split(i4{}, i4{}, ahead{});
+    const int64_t tm = tiles(a.M, 128), tn = tiles(a.N, 128);
+    if (tm * tn > 0x7fffffLL) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(gemm_odd_kernel<T>, dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, (int)tm, (int)tn);
+    return hipGetLastError();
 }
 
 template <Elt T> static hipError_t launch_gemm_type(const GemmArgs &a, hipStream_t st)
