@@ -74,7 +74,11 @@ struct GemmArgs {
 };
 // parts that the contraction is split into, for a product whose partial sums may be kept in a workspace
 int gemm_splits(int64_t M, int64_t N, int64_t kbytes);
+int gemm_columns_splits(int64_t M, int64_t N, int64_t kbytes);
 hipError_t launch_gemm(Elt e, const GemmArgs &a, const char *name, hipStream_t st);
+// The contracted axis down the columns, bf16: x [kbytes / 2][ldx], w [kbytes / 2][ldw], rows at whole 16
+// bytes, N in eights.
+hipError_t launch_gemm_columns(const GemmArgs &a, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs &a, hipStream_t st);
 hipError_t launch_gemm_f32(const GemmArgs &a, hipStream_t st);
 hipError_t launch_gemm_e4m3(const GemmArgs &a, hipStream_t st);

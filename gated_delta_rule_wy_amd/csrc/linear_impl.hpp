@@ -335,6 +335,12 @@ static __device__ __forceinline__ int swap_of(int row) { return (row >> 1) & 7; 
 // the next. So the matrix cores wait neither at the barrier nor for LDS, and a
 // step's loads have a whole step to land.
 //
+// TR: the contracted axis goes down the operands' columns (a gradient's sum over rows,
+// bf16 alone). A step is 64 of its rows, BM elements of each of x's and BN of w's; the bytes are the
+// same. Chunk c of row k lies at position c ^ 2 (k % 8), and LDS is read by the instruction that
+// hands 16 lanes the columns of 4 x 16 elements, so nothing has to be turned in memory
+// before. (Its lanes' 32 bytes of eight rows fall on different banks.)
+//
 // Workgroups stay and go through the tiles; the last two steps of a tile bring
 // the first two of the next, so the sums' way to memory overlaps with them.
 // The kernel's first argument, where it lies in memory.
@@ -482,7 +488,7 @@ static __device__ __forceinline__ void finish_blocks(const GemmArgs &e, int64_t 
 // Waits for what this wave has under way from memory to LDS (a barrier alone does not).
 static __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-template <Elt T, int BM, int BN, int WM, int WN>
+template <Elt T, int BM, int BN, int WM, int WN, bool TR>
 __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2))) void gemm_tile_kernel(GemmArgs a, int tm,
                                                                                                        int tn)
 {
@@ -490,6 +496,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
     constexpr int RX = BM / 8 / NW, RW = BN / 8 / NW;                   // groups of 8 rows each wave brings
     constexpr int BUF = (BM + BN) * kStep;
     static_assert(RX * 8 * NW == BM && RW * 8 * NW == BN && NW % 2 == 0, "whole groups a wave, in one half of 16 rows");
+    static_assert(!TR || (T == Elt::kBf16 && BM >= 128 && BN >= 128 && MB * 32 == 64), "rows of 16 chunks and more, read 16 bits a time");
     __shared__ __attribute__((aligned(1024))) char lds[2 * BUF + NW * 4096];
     const int lane = threadIdx.x & 63, wv = wave_id();
     const int wm = wv % WM, wn = wv / WM;
@@ -512,14 +519,32 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
     // chunk that belongs at position lane % 8. Reads go through buffer descriptors that
     // end with the operand, and what lies beyond an end arrives as zeros: rows behind the
     // last one, and chunks behind a row's end, whose offset is made too large.
-    const uint32_t gx = (uint32_t)(NW * 8) * (uint32_t)a.ldx, gw = (uint32_t)(NW * 8) * (uint32_t)a.ldw;
+    // TR: of every NW-th KB of 1 KB pieces, each a few of the step's rows.
+    constexpr int CX = BM / 8, CW = BN / 8;   // TR: chunks of a step's row
+    const uint32_t gx = (uint32_t)(NW * (TR ? 64 / CX : 8)) * (uint32_t)a.ldx, gw = (uint32_t)(NW * (TR ? 64 / CW : 8)) * (uint32_t)a.ldw;
     uint32_t vx, vw;               // bytes from the step's first
     int cof, ox, ow;               // its chunk in a row; in LDS: this lane's rows of x and w, at its chunk
+    int ox2 = 0, ow2 = 0;          // TR: the next four rows
     auto place = [&]() GDN2_INLINE {
         // (lane from where the compiler cannot see it, here and in the epilogue: what is made
         // of it would otherwise be kept in registers through both)
         int l = lane;
         asm volatile("" : "+v"(l));
+        if constexpr (TR) {
+            const int rx = wv * (64 / CX) + l / CX, rw = wv * (64 / CW) + l / CW;
+            vx = (uint32_t)rx * (uint32_t)a.ldx + ((l % CX) ^ (2 * (rx & 7))) * 16;
+            vw = (uint32_t)rw * (uint32_t)a.ldw + ((l % CW) ^ (2 * (rw & 7))) * 16;
+            cof = 0;
+            // lane t of 16 reads 8 bytes of row t / 4 and is given column t; 32 columns by the half wave, rows
+            // 8 (l / 32) and on by the halves. A block's chunks differ from the first's by xor.
+            const int t = l & 15, k = 8 * (l >> 5) + t / 4, c = (l >> 4 & 1) * 2 + (t & 3) / 2, b = (t & 1) * 8;
+            const int cx = wm * (BM / WM / 8) + c, cw = wn * (BN / WN / 8) + c;
+            ox = k * (BM * 2) + (cx ^ (2 * (t / 4))) * 16 + b;
+            ox2 = (k + 4) * (BM * 2) + (cx ^ (2 * (t / 4 + 4))) * 16 + b;
+            ow = BM * kStep + k * (BN * 2) + (cw ^ (2 * (t / 4))) * 16 + b;
+            ow2 = BM * kStep + (k + 4) * (BN * 2) + (cw ^ (2 * (t / 4 + 4))) * 16 + b;
+            return;
+        }
         const int grow = l >> 3;
         cof = ((l & 7) ^ swap_of((wv & 1) * 8 + grow)) * 16;
         vx = (uint32_t)(wv * 8 + grow) * (uint32_t)a.ldx + cof;
@@ -536,13 +561,13 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
         const Unit q = unit_of(jf);
         fs = q.s0;
         fs1 = q.s1;
-        atx = q.m0 * a.ldx + (int64_t)fs * kStep;
-        atw = q.n0 * a.ldw + (int64_t)fs * kStep;
+        atx = TR ? q.m0 * 2 + (int64_t)fs * (64 * a.ldx) : q.m0 * a.ldx + (int64_t)fs * kStep;
+        atw = TR ? q.n0 * 2 + (int64_t)fs * (64 * a.ldw) : q.n0 * a.ldw + (int64_t)fs * kStep;
     };
     auto fetch = [&](char *buf) GDN2_INLINE {
         if (jf >= count) return;
-        const bool in = fs * kStep + cof < (int)a.kbytes;
-        const auto bx = buffer_at(a.x, atx, a.M * a.ldx), bw = buffer_at(a.w, atw, a.N * a.ldw);
+        const bool in = TR || fs * kStep + cof < (int)a.kbytes;
+        const auto bx = buffer_at(a.x, atx, (TR ? a.kbytes / 2 : a.M) * a.ldx), bw = buffer_at(a.w, atw, (TR ? a.kbytes / 2 : a.N) * a.ldw);
         auto bring = [&](__amdgpu_buffer_rsrc_t from, uint32_t v, char *to) GDN2_INLINE {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16,
                                                      (int)(in ? v : kBeyond), 0, 0, 0);
@@ -551,8 +576,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
         for (int i = 0; i < RX; ++i) bring(bx, vx + i * gx, buf + (i * NW + wv) * 1024);
 #pragma unroll
         for (int i = 0; i < RW; ++i) bring(bw, vw + i * gw, buf + BM * kStep + (i * NW + wv) * 1024);
-        atx += kStep;
-        atw += kStep;
+        atx += TR ? 64 * a.ldx : kStep;
+        atw += TR ? 64 * a.ldw : kStep;
         if (++fs == fs1) {
             jf += stride;
             aim();
@@ -565,6 +590,26 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
     u4 fw[2][2][2], fx[2][MB][2];   // [phase or half % 2][block][chunk]
     auto read = [&](const char *buf, auto phase) GDN2_INLINE {
         constexpr int P = decltype(phase)::value, H = P / NP, J = P % NP * 2;
+        if constexpr (TR) {
+            // 16 of the step's rows: the columns of a block of 32, four rows of a lane's eight at a time
+            auto columns = [&](int first, int second, int block, int pitch, int rows) GDN2_INLINE {
+                typedef short s4 __attribute__((ext_vector_type(4)));
+                typedef __attribute__((address_space(3))) s4 lds4;
+                struct P { s4 a[2]; } p;
+                p.a[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(buf + rows * pitch + (first ^ (block * 64))));
+                p.a[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(buf + rows * pitch + (second ^ (block * 64))));
+                return __builtin_bit_cast(u4, p);
+            };
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) fw[P & 1][j][c] = columns(ow, ow2, J + j, BN * 2, H * 32 + c * 16);
+                if constexpr (J == 0)
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) fx[H][i][c] = columns(ox, ox2, i, BM * 2, H * 32 + c * 16);
+            }
+            return;
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -788,7 +833,7 @@ template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a
         if (tm * tn > 0x7fffffLL) return hipErrorInvalidConfiguration;
         // as many workgroups as there is room for (one or two a compute unit), a multiple of the XCDs'
         const int64_t grid = std::min<int64_t>((tm * tn * a.splits + 7) / 8 * 8, WM * WN == 8 ? 256 : 512);
-        hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, WM, WN>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, st, a, (int)tm,
+        hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, WM, WN, false>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, st, a, (int)tm,
                            (int)tn);
         return hipGetLastError();
     };
