@@ -337,9 +337,10 @@ static __device__ __forceinline__ int swap_of(int row) { return (row >> 1) & 7; 
 //
 // TR: the contracted axis goes down the operands' columns (a gradient's sum over rows,
 // bf16 alone). A step is 64 of its rows, BM elements of each of x's and BN of w's; the bytes are the
-// same. Chunk c of row k lies at position c ^ 2 (k % 8), and LDS is read by the instruction that
+// same. Chunk c of row k lies at position c ^ 4 (k % 4), and LDS is read by the instruction that
 // hands 16 lanes the columns of 4 x 16 elements, so nothing has to be turned in memory
-// before. (Its lanes' 32 bytes of eight rows fall on different banks.)
+// before. (32 lanes read 64 bytes of each of four rows, which fall on
+// different banks.)
 //
 // Workgroups stay and go through the tiles; the last two steps of a tile bring
 // the first two of the next, so the sums' way to memory overlaps with them.
@@ -524,7 +525,6 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
     const uint32_t gx = (uint32_t)(NW * (TR ? 64 / CX : 8)) * (uint32_t)a.ldx, gw = (uint32_t)(NW * (TR ? 64 / CW : 8)) * (uint32_t)a.ldw;
     uint32_t vx, vw;               // bytes from the step's first
     int cof, ox, ow;               // its chunk in a row; in LDS: this lane's rows of x and w, at its chunk
-    int ox2 = 0, ow2 = 0;          // TR: the next four rows
     auto place = [&]() GDN2_INLINE {
         // (lane from where the compiler cannot see it, here and in the epilogue: what is made
         // of it would otherwise be kept in registers through both)
@@ -532,17 +532,15 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
         asm volatile("" : "+v"(l));
         if constexpr (TR) {
             const int rx = wv * (64 / CX) + l / CX, rw = wv * (64 / CW) + l / CW;
-            vx = (uint32_t)rx * (uint32_t)a.ldx + ((l % CX) ^ (2 * (rx & 7))) * 16;
-            vw = (uint32_t)rw * (uint32_t)a.ldw + ((l % CW) ^ (2 * (rw & 7))) * 16;
+            vx = (uint32_t)rx * (uint32_t)a.ldx + ((l % CX) ^ (4 * (rx & 3))) * 16;
+            vw = (uint32_t)rw * (uint32_t)a.ldw + ((l % CW) ^ (4 * (rw & 3))) * 16;
             cof = 0;
             // lane t of 16 reads 8 bytes of row t / 4 and is given column t; 32 columns by the half wave, rows
             // 8 (l / 32) and on by the halves. A block's chunks differ from the first's by xor.
             const int t = l & 15, k = 8 * (l >> 5) + t / 4, c = (l >> 4 & 1) * 2 + (t & 3) / 2, b = (t & 1) * 8;
             const int cx = wm * (BM / WM / 8) + c, cw = wn * (BN / WN / 8) + c;
-            ox = k * (BM * 2) + (cx ^ (2 * (t / 4))) * 16 + b;
-            ox2 = (k + 4) * (BM * 2) + (cx ^ (2 * (t / 4 + 4))) * 16 + b;
-            ow = BM * kStep + k * (BN * 2) + (cw ^ (2 * (t / 4))) * 16 + b;
-            ow2 = BM * kStep + (k + 4) * (BN * 2) + (cw ^ (2 * (t / 4 + 4))) * 16 + b;
+            ox = k * (BM * 2) + (cx ^ (4 * (t / 4))) * 16 + b;
+            ow = BM * kStep + k * (BN * 2) + (cw ^ (4 * (t / 4))) * 16 + b;
             return;
         }
         const int grow = l >> 3;
@@ -592,21 +590,21 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
         constexpr int P = decltype(phase)::value, H = P / NP, J = P % NP * 2;
         if constexpr (TR) {
             // 16 of the step's rows: the columns of a block of 32, four rows of a lane's eight at a time
-            auto columns = [&](int first, int second, int block, int pitch, int rows) GDN2_INLINE {
+            auto columns = [&](int at, int block, int pitch, int rows) GDN2_INLINE {
                 typedef short s4 __attribute__((ext_vector_type(4)));
                 typedef __attribute__((address_space(3))) s4 lds4;
                 struct P { s4 a[2]; } p;
-                p.a[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(buf + rows * pitch + (first ^ (block * 64))));
-                p.a[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(buf + rows * pitch + (second ^ (block * 64))));
+                p.a[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(buf + rows * pitch + (at ^ (block * 64))));
+                p.a[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(buf + (rows + 4) * pitch + (at ^ (block * 64))));
                 return __builtin_bit_cast(u4, p);
             };
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) fw[P & 1][j][c] = columns(ow, ow2, J + j, BN * 2, H * 32 + c * 16);
+                for (int j = 0; j < 2; ++j) fw[P & 1][j][c] = columns(ow, J + j, BN * 2, H * 32 + c * 16);
                 if constexpr (J == 0)
 #pragma unroll
-                    for (int i = 0; i < MB; ++i) fx[H][i][c] = columns(ox, ox2, i, BM * 2, H * 32 + c * 16);
+                    for (int i = 0; i < MB; ++i) fx[H][i][c] = columns(ox, i, BM * 2, H * 32 + c * 16);
             }
             return;
         }
