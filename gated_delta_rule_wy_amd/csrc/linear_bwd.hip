@@ -7,7 +7,7 @@
 // are turned around first, and w, which is small, always is for dx. The pass over dy and
 // the forward's z that forms dz turns it as well, and leaves db's partial rows (added by
 // column_sums.hip in a fixed order); without an activation and a bias there is none. It is
-// bound by memory. (32768 x 2048 x 2048 bf16, sigmoid: 711 us with x and dz turned, NEWUS without.)
+// bound by memory. (32768 x 2048 x 2048 bf16, sigmoid: 711 us with x and dz turned, 623 without.)
 //
 // dz is fp32 in that pass, where db takes it, and is rounded to the operands' type for
 // the products: the matrix instructions take no wider bf16 operand, and the
@@ -23,7 +23,10 @@ namespace gdn2 {
 // act'(z), with e = exp(-|z|) so that nothing cancels for large |z|
 static __device__ __forceinline__ float sigmoid_slope(float u, float &s)
 {
-    const float e = expf(-fabsf(u)), d = 1.f / (1.f + e);
+    // (the exponent's product is rounded once, as u itself was; the reciprocal is off by its last bit)
+    // (the instruction gives 0 below 2^-126, which z may still make a number of: 64 steps up and down again)
+    const float p = fabsf(u) * -1.44269504f, up = p < -100.f ? 64.f : 0.f;
+    const float e = __builtin_amdgcn_exp2f(p + up) * (p < -100.f ? 0x1p-64f : 1.f), d = __builtin_amdgcn_rcpf(1.f + e);
     s = u < 0.f ? e * d : d;
     return e * d * d;
 }
@@ -124,23 +127,97 @@ template <typename In, typename T> __global__ __launch_bounds__(256) void turn_k
     }
 }
 
-// workgroups along the rows: eight a compute unit in all
-static int turn_rows(int64_t R, int C)
+// The same without anything turned: TX lanes take 8 TX neighbours of a row (whole
+// pieces of memory: 32768 x 2048 bf16 94 us in tiles, 75 so, 5.4 TB/s), four rows at a time.
+template <typename In, typename T, int TX> __global__ __launch_bounds__(256) void dz_kernel(TurnArgs a)
 {
-    const int64_t across = (C + 63) / 64;
-    return (int)std::max<int64_t>(1, std::min((R + 63) / 64, 2048 / across));
+    constexpr int TY = 256 / TX, ROWS = 4;
+    __shared__ float sums[TY > 1 ? TY : 1][TX * 8 + 4];
+    const int p = threadIdx.x % TX, y = threadIdx.x / TX, c = (blockIdx.x * TX + p) * 8, cnt = a.C - c;
+    float db[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t r0 = (int64_t)blockIdx.y * (TY * ROWS); r0 < a.R && c < a.Cp; r0 += (int64_t)gridDim.y * (TY * ROWS)) {
+        Pack8<In> x[ROWS];
+        Pack8<T> z[ROWS];
+#pragma unroll
+        for (int h = 0; h < ROWS; ++h) {
+            const int64_t r = r0 + h * TY + y, at = r * a.C + c;
+            const int n = r < a.R ? cnt : 0;
+            z[h].zero();
+            if (n >= 8) {
+                x[h].template load<false, true>((const In *)a.in + at);
+                if (a.preact) z[h].template load<false, true>((const T *)a.preact + at);
+            } else {
+                x[h].load_some((const In *)a.in + at, n);
+                if (a.preact) z[h].load_some((const T *)a.preact + at, n);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < ROWS; ++h) {
+            const int64_t r = r0 + h * TY + y;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = x[h].get(i);
+                if (a.preact) v[i] *= slope_of(a.act, z[h].get(i));
+                db[i] += v[i];
+            }
+            if (a.copy && r < a.R) store8<true>((T *)a.copy + r * a.Cp + c, v);
+        }
+    }
+    if (!a.partial) return;
+    if constexpr (TY > 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[y][p * 8 + i] = db[i];
+        __syncthreads();
+        for (int i = threadIdx.x; i < TX * 8; i += 256) {
+            const int at = blockIdx.x * TX * 8 + i;
+            if (at < a.C) {
+                float s = 0.f;
+#pragma unroll
+                for (int t = 0; t < TY; ++t) s += sums[t][i];
+                a.partial[(int64_t)blockIdx.y * a.C + at] = s;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < cnt) a.partial[(int64_t)blockIdx.y * a.C + c + i] = db[i];
+    }
+}
+
+// How the rows of dz are shared: lanes across, workgroups across and down. With something
+// turned, tiles, eight workgroups a compute unit in all; without, four.
+struct DzShape { int tx, across, down; };
+static DzShape dz_shape(int64_t R, int C, bool turned)
+{
+    DzShape d;
+    d.tx = turned || C <= 64 ? 8 : C <= 256 ? 32 : C <= 1024 ? 128 : 256;
+    d.across = (C + d.tx * 8 - 1) / (d.tx * 8);
+    const int64_t rows = turned ? 64 : 256 / d.tx * 4;
+    d.down = (int)std::max<int64_t>(1, std::min((R + rows - 1) / rows, (turned ? 2048 : 1024) / (int64_t)d.across));
+    return d;
 }
 
 static void turn(TurnArgs a, bool in_bf16, bool bf16, const char *name, hipStream_t st)
 {
-    const dim3 grid((a.C + 63) / 64, turn_rows(a.R, a.C));
+    const DzShape d = dz_shape(a.R, a.C, a.turned);
+    const dim3 grid(d.across, d.down);
+    auto run = [&](auto in, auto out) {
+        using In = decltype(in);
+        using T = decltype(out);
+        if (a.turned) hipLaunchKernelGGL((turn_kernel<In, T>), grid, dim3(256), 0, st, a);
+        else if (d.tx == 8) hipLaunchKernelGGL((dz_kernel<In, T, 8>), grid, dim3(256), 0, st, a);
+        else if (d.tx == 32) hipLaunchKernelGGL((dz_kernel<In, T, 32>), grid, dim3(256), 0, st, a);
+        else if (d.tx == 128) hipLaunchKernelGGL((dz_kernel<In, T, 128>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((dz_kernel<In, T, 256>), grid, dim3(256), 0, st, a);
+    };
     prof_before(name, st);
     if (bf16) {
-        if (in_bf16) hipLaunchKernelGGL((turn_kernel<uint16_t, uint16_t>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((turn_kernel<float, uint16_t>), grid, dim3(256), 0, st, a);
+        if (in_bf16) run(uint16_t(0), uint16_t(0));
+        else run(0.f, uint16_t(0));
     } else {
-        if (in_bf16) hipLaunchKernelGGL((turn_kernel<uint16_t, float>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((turn_kernel<float, float>), grid, dim3(256), 0, st, a);
+        if (in_bf16) run(uint16_t(0), 0.f);
+        else run(0.f, 0.f);
     }
     prof_after(st);
 }
@@ -175,7 +252,7 @@ static BwdLayout bwd_layout(int64_t M, int N, int K, int act, bool bf16, bool dy
     if (dw && (l.dw_splits = l.columns ? gemm_columns_splits(N, K, M * e) : gemm_splits(N, K, Mp * e)) > 1)
         part = std::max(part, (size_t)l.dw_splits * N * Kp * 4);
     if (part) l.partial = take(part);
-    if (db) l.db = take((size_t)turn_rows(M, N) * N * 4);
+    if (db) l.db = take((size_t)dz_shape(M, N, dw && !l.columns).down * N * 4);
     return l;
 }
 
@@ -258,7 +335,7 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a, hipStream_t st)
         c.part[0] = (const float *)(ws + l.db);
         c.out0[0] = a.dbias;
         c.n0[0] = a.N;
-        c.parts = turn_rows(a.M, a.N);
+        c.parts = dz_shape(a.M, a.N, a.dweight && !l.columns).down;
         c.jobs = 1;
         return launch_column_sums(c, "gdn2_linear_bwd_db", st);
     }
