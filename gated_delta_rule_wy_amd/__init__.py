@@ -1097,17 +1097,17 @@ def _tensor_list(tensors, name):
     if not tensors:
         raise ValueError(f'{name}: no tensors')
     n, dev = len(tensors), _gpu(tensors[0], name)
-    ptrs, sizes, types = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    types = [_CODES.get(t.dtype) for t in tensors]
+    if None in types:
+        i = types.index(None)
+        raise TypeError(f'{name}[{i}]: unsupported dtype {tensors[i].dtype} (bfloat16 or float32)')
     for i, t in enumerate(tensors):
-        code = _CODES.get(t.dtype)
-        if code is None:
-            raise TypeError(f'{name}[{i}]: unsupported dtype {t.dtype} (bfloat16 or float32)')
         if t.device != dev:
             raise ValueError(f'{name}[{i}]: expected device {dev}, got {t.device}')
         if not t.is_contiguous():
             raise ValueError(f'{name}[{i}]: must be contiguous')
-        ptrs[i], sizes[i], types[i] = t.data_ptr(), t.numel(), code
-    return tensors, dev, ptrs, sizes, types
+    return (tensors, dev, (ctypes.c_void_p * n)(*map(_data_ptr, tensors)), (ctypes.c_int64 * n)(*map(torch.Tensor.numel, tensors)),
+            (ctypes.c_int32 * n)(*types))
 
 
 def grad_norm(grads, *, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
