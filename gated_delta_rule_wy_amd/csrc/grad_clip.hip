@@ -21,10 +21,10 @@ namespace gdn2 {
 
 constexpr int kTensors = 64, kThreads = 256, kRounds = 8, kPiece = kThreads * 8 * kRounds;
 
-// Most workgroups of the scaling: many short ones keep reads and writes even (235 M bf16 to fp32,
+// Most workgroups of the scaling: many short ones keep reads and writes even (206 M bf16 to fp32,
 // both kernels: 358 us with 1024 of them and two rounds of loads each under way, 285 with 16384). Up to
 // kCached bytes in all what the norm read is in the caches, and read from there; more of it
-// is read past them (23 M floats in and out 20 us instead of 27, 705 M bytes 285 instead of 317).
+// is read past them (7 M floats 20 us instead of 27, 206 M bf16 to fp32 285 instead of 317).
 constexpr int kScaleGrid = 16 * kClipGrid;
 constexpr int64_t kCached = 128 << 20;
 

@@ -820,9 +820,8 @@ template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a
     auto tiles = [](int64_t rows, int b) { return (rows + b - 1) / b; };
     auto split = [&](auto mb, auto nb, auto d) {
         constexpr int MB = decltype(mb)::value, NB = decltype(nb)::value, D = decltype(d)::value;
-        const int64_t gx = tiles(a.N, NB * 16), gy = tiles(a.M, MB * 16);
-        if (gy > 65535 || gx * gy > 0x7fffffLL) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL((gemm_split_kernel<T, MB, NB, D, ODD>), dim3((unsigned)gx, (unsigned)gy), dim3(kWaves * 64), 0, st, a);
+        hipLaunchKernelGGL((gemm_split_kernel<T, MB, NB, D, ODD>), dim3((unsigned)tiles(a.N, NB * 16), (unsigned)tiles(a.M, MB * 16)),
+                           dim3(kWaves * 64), 0, st, a);
         return hipGetLastError();
     };
     auto tiled = [&](auto bm, auto bn, auto wm, auto wn) {
@@ -841,26 +840,32 @@ template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a
     using i64 = std::integral_constant<int, 64>;
     using i128 = std::integral_constant<int, 128>;
     using i256 = std::integral_constant<int, 256>;
-    // fp32's matrix instructions take so long that one step ahead is enough, and that operands
-    // from the L2 keep up with them: small blocks, which leave no compute unit idle at the end, are used far longer
-    // (1024^3: 23 us, 25 with a step ahead, 39 in tiles).
     constexpr bool kSlow = T == Elt::kF32;
-    using ahead = std::conditional_t<kSlow, i1, i2>;
+    const bool whole = !ODD && a.N % 8 == 0;
+    // The smallest blocks of the waves that share the contraction, if they give no compute unit
+    // a second workgroup: the chip is as full as it can be, and most loads are under way (bf16, K =
+    // 2048, us in blocks of 16 x 16, 16 x 32, 32 x 32, 32 x 64: 32 x 2048 6.3, 7.7, 9.5, 14.0; 64 x 2048 9.8, 7.8,
+    // 9.5, 14.0; 32 x 8192 16.8, 13.0, 9.9, 14.4; 64 x 8192 30.6, 23.4, 17.7, 14.7, and 20 in tiles). fp32
+    // takes some workgroups more: half the compute units would have none of the next size.
+    if (a.splits == 1) {
+        auto blocks = [&](int rows, int cols) { return tiles(a.M, rows) * tiles(a.N, cols); };
+        if (blocks(16, 16) <= 256) return split(i1{}, i1{}, i4{});
+        if (blocks(16, 32) <= 256) return split(i1{}, i2{}, i4{});
+        if (blocks(32, 32) <= 256) return split(i2{}, i2{}, i4{});
+        if (blocks(32, 64) <= (kSlow ? 384 : 256)) return split(i2{}, i4{}, std::conditional_t<kSlow, i1, i2>{});
+    }
     // Rows that LDS can take whole chunks of, and y in whole eights: tiles, the larger ones where they
     // fill the chip (bf16, K = N = 2048: 1024 rows 18 us in tiles of 128 x 64, 35 in blocks
-    // of the waves that share the contraction; 4096 rows 35 us in 128 x 128, 46 in 128 x 64; 512 rows 16 and 18, 256
-    // rows 16 and 15).
-    const bool whole = !ODD && a.N % 8 == 0;
+    // of the waves that share the contraction; 4096 rows 35 us in 128 x 128, 46 in 128 x 64; 512 rows 16 and 18).
     if (whole && tiles(a.M, 256) * tiles(a.N, 256) * a.splits >= 192) return tiled(i256{}, i256{}, i4{}, i2{});
     if (whole && tiles(a.M, 128) * tiles(a.N, 128) * a.splits >= (kSlow ? 512 : 256)) return tiled(i128{}, i128{}, i2{}, i2{});
     if (whole && (a.splits > 1 || (!kSlow && tiles(a.M, 128) * tiles(a.N, 64) >= 128))) return tiled(i128{}, i64{}, i4{}, i1{});
-    if (a.M <= 16) return split(i1{}, i1{}, i4{});
-    if (a.M <= 32) return split(i2{}, i1{}, i4{});
-    if (a.M <= 64) return split(i4{}, i1{}, i4{});
-    // the largest blocks that give every compute unit a workgroup (fp32: most of them)
-    if (tiles(a.M, 32) * tiles(a.N, 64) < (kSlow ? 128 : 256)) return split(i2{}, i2{}, i4{});
-    if (tiles(a.M, 64) * tiles(a.N, 64) < (kSlow ? 192 : 256)) return split(i2{}, i4{}, ahead{});
-    if (kSlow || tiles(a.M, 64) * tiles(a.N, 64) <= 512) return split(i4{}, i4{}, ahead{});
+    // fp32's matrix instructions take so long that one step ahead is enough, and that operands
+    // from the L2 keep up with them: small blocks, which leave no compute unit idle at the end, are used far longer
+    // (1024^3: 23 us, 25 with a step ahead, 39 in tiles).
+    const int64_t blocks = tiles(a.M, 64) * tiles(a.N, 64);
+    if (blocks <= 512 || (kSlow && tiles(a.M, 64) <= 65535 && blocks <= 0x7fffffLL))
+        return split(i4{}, i4{}, std::conditional_t<kSlow, i1, i2>{});
     const int64_t tm = tiles(a.M, 128), tn = tiles(a.N, 128);
     if (tm * tn > 0x7fffffLL) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(gemm_odd_kernel<T>, dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, (int)tm, (int)tn);

@@ -327,3 +327,23 @@ def test_binding_refuses():
             (ValueError, (y, x, w), dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)))]:
         with pytest.raises(err):
             gdn2.linear_bwd(*args, **kw)
+
+
+@pytest.mark.parametrize('dtype', ['bf16', 'f32', 'e4m3'])
+def test_more_rows_than_a_grid_has_blocks(dtype):
+    """2^22 rows and a few: 64 at a time are more than a launch's second axis holds."""
+    M, N, K = 2 ** 22 + 77, 3, 2
+    print(f'[many rows] {M}x{N}x{K} {dtype}', flush=True)
+    c = Case(5, M, N, K, dtype)
+    oref.check('y', back(c.run('silu')[0]), c.want('silu')[0])
+
+
+def test_gradient_of_the_most_rows():
+    M, N, K = 2 ** 22, 2, 3
+    print(f'[most rows] {M}x{N}x{K}', flush=True)
+    g = torch.Generator().manual_seed(6)
+    dy, x, w = (torch.randn(s, generator=g) for s in ((M, N), (M, K), (N, K)))
+    out = gdn2.linear_bwd(dy.to(DEV), x.to(DEV), w.to(DEV))
+    want = ref.linear_bwd(dy.numpy(), x.numpy(), w.numpy(), None, 'none')
+    for k in ('x', 'weight', 'bias'):
+        oref.check(k, back(out[k]), want[k])
