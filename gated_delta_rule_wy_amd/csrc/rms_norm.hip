@@ -22,6 +22,26 @@ namespace gdn2 {
 
 constexpr float kTopE4m3 = 448.f, kLeastScale = 1.17549435e-38f;
 
+// A row's scale from its largest |y|, and the row's elements by it. y / scale = y 448 / top is taken with
+// the roundings of its factors beside it and rounded once: an element next to a border between two e4m3 numbers
+// falls to the right side of it (rstd's own error is in top as well). No slower: 65536 x 2048 157 us, 158 without.
+struct RowScale {
+    float scale, by, rest;   // 448 / top = by + rest
+    __device__ __forceinline__ explicit RowScale(float top)
+    {
+        const float own = top / kTopE4m3;
+        scale = fmaxf(own, kLeastScale);
+        by = own >= kLeastScale ? kTopE4m3 / top : 1.f / scale;
+        // (none of it where the row holds infinities or is scaled by the least scale, a power of two)
+        rest = own >= kLeastScale && by > 0.f ? fmaf(-by, top, kTopE4m3) * (by * (1.f / kTopE4m3)) : 0.f;
+    }
+    __device__ __forceinline__ float operator()(float h, float rstd, float w) const
+    {
+        const float xh = h * rstd, y = xh * w, low = fmaf(fmaf(h, rstd, -xh), w, fmaf(xh, w, -y));
+        return fmaf(y, by, fmaf(low, by, y * rest));
+    }
+};
+
 template <typename In, typename Out, Packs P, int TPR, int E, bool RES>
 __global__ __launch_bounds__((RowShape<TPR>::NT)) void rms_fwd_kernel(
     const In *x, const In *res, const float *__restrict__ weight, Out *y, float *scale, In *sum, int64_t rows, int cols,
@@ -63,23 +83,24 @@ __global__ __launch_bounds__((RowShape<TPR>::NT)) void rms_fwd_kernel(
         if (live && sum)
 #pragma unroll
             for (int e = 0; e < E; ++e) part.store(sum + base, h[e], e);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[e][i] = h[e][i] * rstd * wv[e][i];
         if constexpr (kScaled) {
             float top = 0.f;   // (what a lane holds twice, or beyond the row as zeros, changes nothing)
 #pragma unroll
             for (int e = 0; e < E; ++e)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (P != Packs::kFew || part.mine(e, i)) top = fmaxf(top, fabsf(h[e][i]));
-            const float sc = fmaxf(row_max<TPR>(top, red) / kTopE4m3, kLeastScale), inv = 1.f / sc;
-            if (live && part.p == 0) scale[row] = sc;
+                    if (P != Packs::kFew || part.mine(e, i)) top = fmaxf(top, fabsf(h[e][i] * rstd * wv[e][i]));
+            const RowScale sc(row_max<TPR>(top, red));
+            if (live && part.p == 0) scale[row] = sc.scale;
 #pragma unroll
             for (int e = 0; e < E; ++e)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[e][i] *= inv;
+                for (int i = 0; i < 8; ++i) h[e][i] = sc(h[e][i], rstd, wv[e][i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[e][i] = h[e][i] * rstd * wv[e][i];
         }
         if (live)
 #pragma unroll
@@ -101,17 +122,16 @@ __global__ __launch_bounds__(1024) void rms_fwd_long_kernel(const In *x, const I
         for (int c = threadIdx.x; c < cols; c += 1024) s[0] += at(c) * at(c);
         row_sums<1024>(s, red);
         const float rstd = 1.f / sqrtf(s[0] * inv_n + eps);
-        float inv = 1.f;
+        float top = 0.f;
         if constexpr (sizeof(Out) == 1) {
-            float top = 0.f;
             for (int c = threadIdx.x; c < cols; c += 1024) top = fmaxf(top, fabsf(at(c) * rstd * weight[c]));
-            const float sc = fmaxf(row_max<1024>(top, red) / kTopE4m3, kLeastScale);
-            inv = 1.f / sc;
-            if (threadIdx.x == 0) scale[r] = sc;
+            top = row_max<1024>(top, red);
         }
+        const RowScale sc(top);
+        if (sizeof(Out) == 1 && threadIdx.x == 0) scale[r] = sc.scale;
         for (int c = threadIdx.x; c < cols; c += 1024) {
-            const float h = at(c), o = h * rstd * weight[c];
-            store1(y + base + c, sizeof(Out) == 1 ? o * inv : o);
+            const float h = at(c);
+            store1(y + base + c, sizeof(Out) == 1 ? sc(h, rstd, weight[c]) : h * rstd * weight[c]);
             if (sum) store1(sum + base + c, h);
         }
     }
