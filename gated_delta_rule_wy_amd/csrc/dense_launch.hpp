@@ -79,6 +79,10 @@ hipError_t launch_gemm(Elt e, const GemmArgs &a, const char *name, hipStream_t s
 // The contracted axis down the columns, bf16: x [kbytes / 2][ldx], w [kbytes / 2][ldw], rows at whole 16
 // bytes, N in eights.
 hipError_t launch_gemm_columns(const GemmArgs &a, hipStream_t st);
+// Whether a product in fp32 takes w (and, with turned_x, x) [count][N] ([count][M]) as they lie, and that product: a.kbytes
+// is 4 count then, the rows of an x that is not turned are whole chunks.
+bool gemm_columns_f32(int64_t M, int64_t N, int64_t count, bool turned_x);
+hipError_t launch_gemm_columns_f32(const GemmArgs &a, bool turned_x, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs &a, hipStream_t st);
 hipError_t launch_gemm_f32(const GemmArgs &a, hipStream_t st);
 hipError_t launch_gemm_e4m3(const GemmArgs &a, hipStream_t st);

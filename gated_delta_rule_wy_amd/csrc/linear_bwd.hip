@@ -2,9 +2,9 @@
 //
 //   dz = dy act'(z),  dx = dz w,  dw = dz^T x,  db = sum over rows of dz
 //
-// The products (linear_impl.hpp) contract along rows, or, in bf16 and where rows begin
-// at whole 16 bytes, along columns: dw takes dz and x as they lie then. Otherwise x and dz
-// are turned around first, and w, which is small, always is for dx. The pass over dy and
+// The products (linear_impl.hpp) contract along rows, or along columns: in bf16, where rows
+// begin at whole 16 bytes, dw takes dz and x as they lie then, and in fp32 products that are too few tiles
+// to fill the chip take theirs, dx's w too. Otherwise x and dz are turned around first, and w. The pass over dy and
 // the forward's z that forms dz turns it as well, and leaves db's partial rows (added by
 // column_sums.hip in a fixed order); without an activation and a bias there is none. It is
 // bound by memory. (32768 x 2048 x 2048 bf16, sigmoid: 711 us with x and dz turned, 623 without.)
@@ -225,7 +225,7 @@ static void turn(TurnArgs a, bool in_bf16, bool bf16, const char *name, hipStrea
 // Where the workspace's parts lie.
 struct BwdLayout {
     size_t copy = 0, dzt = 0, xt = 0, wt = 0, partial = 0, db = 0, bytes = 0;
-    bool need_copy, columns;
+    bool need_copy, columns, w_columns;   // dw's operands, dx's w are taken as they lie
     int dx_splits = 1, dw_splits = 1;
 };
 static BwdLayout bwd_layout(int64_t M, int N, int K, int act, bool bf16, bool dy_bf16, bool dx, bool dw, bool db)
@@ -238,7 +238,8 @@ static BwdLayout bwd_layout(int64_t M, int N, int K, int act, bool bf16, bool dy
         l.bytes += (n + 255) / 256 * 256;
         return at;
     };
-    l.columns = dw && bf16 && K % 8 == 0 && M > 0;
+    l.columns = dw && M > 0 && (bf16 ? K % 8 == 0 : gemm_columns_f32(N, K, M, true));
+    l.w_columns = dx && !bf16 && gemm_columns_f32(M, K, N, false);
     // dz where dy is not it, as it stands
     l.need_copy = (dx || l.columns) && (act != kActNone || dy_bf16 != bf16 || N % 8 != 0);
     if (l.need_copy) l.copy = take((size_t)M * Np * e);
@@ -246,10 +247,10 @@ static BwdLayout bwd_layout(int64_t M, int N, int K, int act, bool bf16, bool dy
         l.dzt = take((size_t)N * Mp * e);
         l.xt = take((size_t)Kp * Mp * e);
     }
-    if (dx) l.wt = take((size_t)Kp * Np * e);
+    if (dx && !l.w_columns) l.wt = take((size_t)Kp * Np * e);
     size_t part = 0;
-    if (dx && (l.dx_splits = gemm_splits(M, K, Np * e)) > 1) part = (size_t)l.dx_splits * M * Kp * 4;
-    if (dw && (l.dw_splits = l.columns ? gemm_columns_splits(N, K, M * e) : gemm_splits(N, K, Mp * e)) > 1)
+    if (dx && !l.w_columns && (l.dx_splits = gemm_splits(M, K, Np * e)) > 1) part = (size_t)l.dx_splits * M * Kp * 4;
+    if (dw && (bf16 || !l.columns) && (l.dw_splits = l.columns ? gemm_columns_splits(N, K, M * e) : gemm_splits(N, K, Mp * e)) > 1)
         part = std::max(part, (size_t)l.dw_splits * N * Kp * 4);
     if (part) l.partial = take(part);
     if (db) l.db = take((size_t)dz_shape(M, N, dw && !l.columns).down * N * 4);
@@ -281,22 +282,33 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a, hipStream_t st)
         turn(t, a.dy_bf16, a.bf16, "gdn2_linear_bwd_dz", st);
     }
     if (a.dx && a.M > 0) {
-        TurnArgs t = {};
-        t.in = a.w;
-        t.turned = ws + l.wt;
-        t.R = a.N; t.Rp = Np; t.C = a.K; t.Cp = Kp;
-        turn(t, a.bf16, a.bf16, "gdn2_linear_bwd_turn", st);
         GemmArgs m = {};
         m.x = l.need_copy ? ws + l.copy : a.dy;
-        m.w = ws + l.wt;
-        m.ldx = m.ldw = m.kbytes = (int64_t)Np * e;
+        m.ldx = (int64_t)Np * e;
         m.M = a.M; m.N = a.K;
         m.y = a.dx;
         m.out_bf16 = a.bf16;
         m.partial = (float *)(ws + l.partial);
         m.ldp = Kp;
         m.splits = l.dx_splits;
-        const hipError_t err = launch_gemm(elt, m, "gdn2_linear_bwd_dx", st);
+        hipError_t err;
+        if (l.w_columns) {
+            m.w = a.w;
+            m.ldw = (int64_t)a.K * 4;
+            m.kbytes = (int64_t)a.N * 4;
+            prof_before("gdn2_linear_bwd_dx", st);
+            err = launch_gemm_columns_f32(m, false, st);
+            prof_after(st);
+        } else {
+            TurnArgs t = {};
+            t.in = a.w;
+            t.turned = ws + l.wt;
+            t.R = a.N; t.Rp = Np; t.C = a.K; t.Cp = Kp;
+            turn(t, a.bf16, a.bf16, "gdn2_linear_bwd_turn", st);
+            m.w = ws + l.wt;
+            m.ldw = m.kbytes = (int64_t)Np * e;
+            err = launch_gemm(elt, m, "gdn2_linear_bwd_dx", st);
+        }
         if (err != hipSuccess) return err;
     }
     if (a.dweight) {
@@ -311,11 +323,11 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a, hipStream_t st)
         if (l.columns) {
             m.x = l.need_copy ? ws + l.copy : a.dy;
             m.w = a.x;
-            m.ldx = Np * 2;
-            m.ldw = (int64_t)a.K * 2;
-            m.kbytes = a.M * 2;
+            m.ldx = (int64_t)Np * e;
+            m.ldw = (int64_t)a.K * e;
+            m.kbytes = a.M * e;
             prof_before("gdn2_linear_bwd_dw", st);
-            err = launch_gemm_columns(m, st);
+            err = a.bf16 ? launch_gemm_columns(m, st) : launch_gemm_columns_f32(m, true, st);
             prof_after(st);
         } else {
             TurnArgs t = {};
@@ -365,6 +377,15 @@ int gemm_columns_splits(int64_t M, int64_t N, int64_t kbytes)
     if (s >= 1 && big * s >= 192) return (int)s;
     s = std::min((512 + small - 1) / small, steps / 16);
     return s >= 2 ? (int)s : 1;
+}
+
+bool gemm_columns_f32(int64_t M, int64_t N, int64_t count, bool turned_x)
+{
+    // blocks of 64 x 64 that fill half the chip at least and are too few for tiles; offsets of 32 bits. (Fewer blocks: the
+    // contraction is split into parts instead. 4096 x 512 x 512: 69 us, 108 with dw in its 64 blocks.)
+    const int64_t blocks = ((M + 63) / 64) * ((N + 63) / 64), most = 0x7fffffffLL;
+    return blocks >= 128 && blocks < 2048 && N >= 64 && count * N * 4 < most &&
+           (!turned_x || (M >= 64 && count * ((M + 7) / 8 * 8) * 4 < most));
 }
 
 hipError_t launch_gemm(Elt e, const GemmArgs &a, const char *name, hipStream_t st)

@@ -347,3 +347,39 @@ def test_gradient_of_the_most_rows():
     want = ref.linear_bwd(dy.numpy(), x.numpy(), w.numpy(), None, 'none')
     for k in ('x', 'weight', 'bias'):
         oref.check(k, back(out[k]), want[k])
+
+
+# fp32 whose operands are read down their columns: dx alone, dw alone, both; sums of one to many terms
+@pytest.mark.parametrize('M,N,K', [(1100, 333, 777), (333, 1100, 777), (1000, 1001, 1003), (1554, 777, 1001), (2000, 1, 300),
+                                   (2000, 5, 300), (1, 1500, 400), (17, 1500, 401), (700, 8, 4000), (600, 2000, 2040), (8000, 64, 200)])
+@pytest.mark.parametrize('act,ddtype', [('none', 'f32'), ('silu', 'bf16')])
+def test_gradient_columns_fp32(M, N, K, act, ddtype):
+    print(f'[columns] {M}x{N}x{K} {act} {ddtype}', flush=True)
+    got, want = grad_case(M + K, M, N, K, 'f32', ddtype, act)
+    for n in want:
+        oref.check(n, back(got[n]), want[n])
+
+
+@pytest.mark.parametrize('M,N,K', [(1000, 1001, 1003), (1100, 336, 777), (333, 1104, 779), (64, 2000, 1040)])
+def test_gradient_reads_nothing_beyond_the_tensors(M, N, K):
+    """fp32 operands that are followed by NaN; outputs that are followed by numbers that stay."""
+    print(f'[beyond] {M}x{N}x{K}', flush=True)
+    g = torch.Generator().manual_seed(M)
+    dy, x, w = (torch.randn(s, generator=g) for s in ((M, N), (M, K), (N, K)))
+
+    def inside(t):
+        flat = torch.full((t.numel() + 4096,), float('nan'), device=DEV)
+        flat[:t.numel()] = t.flatten().to(DEV)
+        return flat[:t.numel()].view(t.shape)
+
+    dx, dw = (torch.full((n + 4096,), 7.0, device=DEV) for n in (M * K, N * K))
+    lib, p = gdn2.lib(), lambda t: t.data_ptr()   # noqa: E731
+    need = lib.gdn2_linear_bwd_workspace_bytes(M, K, N, 0, gdn2.GDN2_F32, gdn2.GDN2_F32, 1, 1, 0)
+    ws = torch.full((need + 4096,), 0xff, dtype=torch.uint8, device=DEV)   # (NaN as well)
+    args = [inside(t) for t in (dy, x, w)]
+    lib.gdn2_set_stream(torch.cuda.current_stream().cuda_stream)
+    assert lib.gdn2_linear_bwd(*map(p, args), None, p(dx), p(dw), None, M, K, N, 0, gdn2.GDN2_F32, gdn2.GDN2_F32, p(ws), need) == 0
+    want = ref.linear_bwd(dy.numpy(), x.numpy(), w.numpy(), None, 'none')
+    oref.check('x', back(dx[:M * K].view(M, K)), want['x'])
+    oref.check('weight', back(dw[:N * K].view(N, K)), want['weight'])
+    assert torch.all(dx[M * K:] == 7.0) and torch.all(dw[N * K:] == 7.0) and torch.all(ws[need:] == 0xff)
