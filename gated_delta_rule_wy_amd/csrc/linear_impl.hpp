@@ -221,7 +221,24 @@ __global__ __launch_bounds__(kWaves * 64) void gemm_split_kernel(GemmArgs a)
         const int at = s * kStep + g * 32;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            if constexpr (ODD) {
+            if constexpr (ODD && T == Elt::kF32) {
+                // (fp32 rows of any length begin at whole words; the last step's are asked for one by one)
+                const bool end = (s + 1) * kStep > (int)a.kbytes;
+                auto chunk = [&](const __amdgpu_buffer_rsrc_t &b, uint32_t row) GDN2_INLINE -> u4 {
+                    if (!end) return __builtin_amdgcn_raw_buffer_load_b128(b, (int)(row + (uint32_t)(at + c * 16)), 0, 0);
+                    u4 v;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int e = at + c * 16 + i * 4;
+                        v[i] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)(e < (int)a.kbytes ? row + (uint32_t)e : kBeyond), 0, 0);
+                    }
+                    return v;
+                };
+#pragma unroll
+                for (int j = 0; j < NB; ++j) q.w[j][c] = chunk(bw, (uint32_t)(j * 16 + r) * (uint32_t)a.ldw);
+#pragma unroll
+                for (int i = 0; i < MB; ++i) q.x[i][c] = chunk(bx, (uint32_t)(i * 16 + r) * (uint32_t)a.ldx);
+            } else if constexpr (ODD) {
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
                     q.w[j][c] = load_chunk<T>((const char *)a.w + min(n0 + j * 16 + r, a.N - 1) * a.ldw, at + c * 16, a.kbytes);
