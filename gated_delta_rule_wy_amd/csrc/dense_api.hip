@@ -211,13 +211,16 @@ struct Range {
 };
 }
 
-// Whether an output shares memory with anything but its own gradient, in place.
+// Whether an output shares memory with anything but its own gradient, in place; the norm
+// (written or read) and the workspace (written, or null) among them.
 static int clip_overlap(const void *const *grads, void *const *out, const int64_t *sizes, const int32_t *in_types,
-                        const int32_t *out_types, int count, bool *bad)
+                        const int32_t *out_types, int count, const float *norm, bool norm_given, const void *workspace, bool *bad)
 {
-    Range *r = new (std::nothrow) Range[2 * (size_t)count];
+    Range *r = new (std::nothrow) Range[2 * (size_t)count + 2];
     if (!r) return GDN2_ERR_HIP;
     int n = 0;
+    r[n++] = {(uintptr_t)norm, (uintptr_t)norm + 4, -1, !norm_given};
+    if (workspace) r[n++] = {(uintptr_t)workspace, (uintptr_t)workspace + gdn2_clip_grads_workspace_bytes(), -1, true};
     for (int i = 0; i < count; ++i) {
         if (sizes[i] == 0) continue;
         auto add = [&](const void *p, int type, bool o) {
@@ -282,11 +285,10 @@ int gdn2_clip_grads(const void *const *grads, void *const *out, const int64_t *s
     if (!(max_norm >= 0.f && max_norm <= 3.4e38f) || !norm || (uintptr_t)norm % 4) return GDN2_ERR_INVALID;
     if (workspace && !aligned16(workspace)) return GDN2_ERR_INVALID;
     if (!norm_given && (!workspace || workspace_bytes < gdn2_clip_grads_workspace_bytes())) return GDN2_ERR_WORKSPACE;
-    if (norm == workspace) return GDN2_ERR_INVALID;
-    for (int i = 0; i < count; ++i)
-        if (sizes[i] > 0 && same_memory({norm, workspace}, {grads[i], out[i]})) return GDN2_ERR_INVALID;
     bool bad;
-    if ((st = clip_overlap(grads, out, sizes, dtypes, out_dtypes, count, &bad)) != GDN2_OK) return st;
+    if ((st = clip_overlap(grads, out, sizes, dtypes, out_dtypes, count, norm, norm_given, norm_given ? nullptr : workspace, &bad)) !=
+        GDN2_OK)
+        return st;
     if (bad) return GDN2_ERR_INVALID;
     ClipArgs a = {};
     a.in = grads;

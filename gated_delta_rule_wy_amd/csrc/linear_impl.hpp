@@ -203,7 +203,9 @@ struct Finish8 {
 // A workgroup of eight waves owns 16 MB rows of x and 16 NB of w. Wave i takes the
 // steps i, i + 8, ... straight from memory into the instructions' operands
 // (nothing is used twice that could be shared through LDS), D - 1 of them on their way while
-// one is multiplied, and the waves' sums are added through LDS in wave order.
+// one is multiplied, and the waves' sums are added through LDS in wave order. Bound by the latency of the
+// first loads and the sum where rows are few (bf16 4 x 2048 x 2048 4.7 us, e4m3 256 x 2048 x 2048 9.0), in fp32 by
+// the matrix instructions (4096 x 1001 x 1024 77 us, 109 of 153 TFLOP/s).
 constexpr int kWaves = 8;
 
 template <Elt T, int MB, int NB, int D, bool ODD>
@@ -361,6 +363,12 @@ static __device__ __forceinline__ int swap_of(int row) { return (row >> 1) & 7; 
 //
 // Workgroups stay and go through the tiles; the last two steps of a tile bring
 // the first two of the next, so the sums' way to memory overlaps with them.
+//
+// 65536 x 2048 x 2048 bf16 490 us, with residual 535 (1.03 PFLOP/s); 32768 x 8192 x 2048 e4m3 to bf16 505 (2.18); by
+// columns 2048 x 2048 x 32768 bf16 290 (0.95). A tile of 256 x 256 and 2048 bf16 takes 60 us of its compute unit, 37 in matrix
+// instructions alone, 49 with the reads of LDS, and 49 in fetches alone (33 where the L2 has all): x comes from memory
+// behind the bursts in which y leaves.
+
 // The kernel's first argument, where it lies in memory.
 static __device__ __forceinline__ GemmArgs arguments()
 {
@@ -711,7 +719,9 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
 }
 
 // The same with rows that do not begin at whole chunks or end with them: chunks go
-// through registers, tiles of 128 x 128, 16 x 16 sums an instruction.
+// through registers, tiles of 128 x 128, 16 x 16 sums an instruction. Bound by the loads, which come from any
+// byte (bf16 5000 x 2001 x 2047: 105 us, 0.39 PFLOP/s; 1000 x 2001 x 2047 50 us, 115 in blocks of the waves that
+// share the contraction; 256 x 2001 x 2047 38 and 44, x 501 17 and 13).
 template <Elt T> __global__ __launch_bounds__(256) void gemm_odd_kernel(GemmArgs a, int tm, int tn)
 {
     constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
@@ -880,9 +890,8 @@ template <Elt T, bool ODD> static hipError_t launch_gemm_forms(const GemmArgs &a
     // fp32's matrix instructions take so long that one step ahead is enough, and that operands
     // from the L2 keep up with them: small blocks, which leave no compute unit idle at the end, are used far longer
     // (1024^3: 23 us, 25 with a step ahead, 39 in tiles).
-    const int64_t blocks = tiles(a.M, 64) * tiles(a.N, 64);
-    if (blocks <= 512 || (kSlow && tiles(a.M, 64) <= 65535 && blocks <= 0x7fffffLL))
-        return split(i4{}, i4{}, std::conditional_t<kSlow, i1, i2>{});
+    if constexpr (kSlow)
+        if (tiles(a.M, 64) <= 65535 && tiles(a.M, 64) * tiles(a.N, 64) <= 0x7fffffLL) return split(i4{}, i4{}, i1{});
     const int64_t tm = tiles(a.M, 128), tn = tiles(a.N, 128);
     if (tm * tn > 0x7fffffLL) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(gemm_odd_kernel<T>, dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, (int)tm, (int)tn);

@@ -171,6 +171,13 @@ def test_clip_grads_rejects(kw, status):
     assert clip(**kw) == status
 
 
+@pytest.mark.parametrize('kw', [dict(norm=P + 0x44), dict(norm=2 * P + 0x3c), dict(ws=P - 0x100), dict(ws=2 * P + 0x20),
+                                dict(norm=2 * P + 0x3c, given=1), dict(norm=0x200 + 64)])
+def test_clip_grads_rejects_a_norm_or_workspace_within_what_is_written(kw):
+    assert clip([P, P + 0x40], [2 * P, 2 * P + 0x40], [16, 16], **kw) == INVALID
+
+
+
 def test_binding_refuses_the_cpu_and_wrong_values():
     x, w = torch.zeros(4, 8), torch.zeros(5, 8)
     for call in (lambda: gdn2.linear_fwd(x, w), lambda: gdn2.linear_bwd(torch.zeros(4, 5), x, w),

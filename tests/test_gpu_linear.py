@@ -383,3 +383,46 @@ def test_gradient_reads_nothing_beyond_the_tensors(M, N, K):
     oref.check('x', back(dx[:M * K].view(M, K)), want['x'])
     oref.check('weight', back(dw[:N * K].view(N, K)), want['weight'])
     assert torch.all(dx[M * K:] == 7.0) and torch.all(dw[N * K:] == 7.0) and torch.all(ws[need:] == 0xff)
+
+
+def test_only_the_fp32_gradients_that_are_asked_for():
+    whole, _ = grad_case(12, 1000, 1001, 1003, 'f32', 'f32', 'silu')
+    for flags in ((1, 0, 0), (0, 1, 0), (0, 1, 1)):
+        names = [n for n, f in zip(('x', 'weight', 'bias'), flags) if f]
+        g, _ = grad_case(12, 1000, 1001, 1003, 'f32', 'f32', 'silu', output_x=bool(flags[0]), output_weight=bool(flags[1]),
+                         output_bias=bool(flags[2]))
+        assert sorted(g) == sorted(names) and all(torch.equal(g[n], whole[n]) for n in names)
+
+
+@pytest.mark.parametrize('M,N,K', [(64, 2048, 256), (1000, 1001, 1003), (4999, 500, 255)])
+def test_fp32_captured_twice(M, N, K):
+    """Two captured passes over the same tensors, replayed in turn on another stream than they were captured
+    on, give the eager pass's bits."""
+    c = Case(15, M, N, K, 'f32')
+    x, w, b, r = (t.to(DEV) for t in (c.x, c.w, c.b, c.r))
+    dy = torch.randn_like(r)
+
+    def step():
+        y, z = gdn2.linear_fwd(x, w, b, r, activation='gelu_tanh', output_preact=True)
+        return [y, z, *gdn2.linear_bwd(dy, x, w, z, activation='gelu_tanh').values()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    outs = []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(step())
+    for i in range(3):
+        x.copy_(torch.randn_like(x))
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for g in graphs:
+                g.replay()
+        side.synchronize()
+        want = step()
+        for out in outs:
+            assert all(torch.equal(p, q) for p, q in zip(out, want)), i
