@@ -209,7 +209,8 @@ struct Finish8 {
 constexpr int kWaves = 8;
 
 template <Elt T, int MB, int NB, int D, bool ODD>
-__global__ __launch_bounds__(kWaves * 64) void gemm_split_kernel(GemmArgs a)
+__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(MB * NB == 16 && ODD ? 4 : 1))) void
+gemm_split_kernel(GemmArgs a)
 {
     constexpr int PITCH = NB * 16 + 4;                   // floats a row of the sums (16-byte aligned, banks apart)
     constexpr int ROUNDS = MB * NB > 4 ? 2 : 1, MR = MB / ROUNDS;   // blocks of rows a round through LDS
@@ -219,27 +220,30 @@ __global__ __launch_bounds__(kWaves * 64) void gemm_split_kernel(GemmArgs a)
     const int64_t m0 = (int64_t)blockIdx.y * (MB * 16), n0 = (int64_t)blockIdx.x * (NB * 16);
     const auto bx = buffer_at(a.x, m0 * a.ldx, a.M * a.ldx), bw = buffer_at(a.w, n0 * a.ldw, a.N * a.ldw);
     struct Frags { u4 x[MB][2], w[NB][2]; } f[D];
-    auto load = [&](Frags &q, int s) GDN2_INLINE {
+    // (part: whether the step may be one that ends within 128 bytes, and is then read with more care)
+    auto load = [&](Frags &q, int s, auto part) GDN2_INLINE {
         const int at = s * kStep + g * 32;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             if constexpr (ODD && T == Elt::kF32) {
                 // (fp32 rows of any length begin at whole words; the last step's are asked for one by one)
-                const bool end = (s + 1) * kStep > (int)a.kbytes;
+                const bool end = decltype(part)::value && (s + 1) * kStep > (int)a.kbytes;
                 auto chunk = [&](const __amdgpu_buffer_rsrc_t &b, uint32_t row) GDN2_INLINE -> u4 {
                     if (!end) return __builtin_amdgcn_raw_buffer_load_b128(b, (int)(row + (uint32_t)(at + c * 16)), 0, 0);
-                    u4 v;
+                    u4 v;   // (behind the row's end are the next row's first words, or the buffer's zeros)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int e = at + c * 16 + i * 4;
-                        v[i] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)(e < (int)a.kbytes ? row + (uint32_t)e : kBeyond), 0, 0);
+                        const uint32_t word = __builtin_amdgcn_raw_buffer_load_b32(b, (int)(row + (uint32_t)(at + c * 16)) + i * 4, 0, 0);
+                        v[i] = at + c * 16 + i * 4 < (int)a.kbytes ? word : 0u;
                     }
                     return v;
                 };
 #pragma unroll
                 for (int j = 0; j < NB; ++j) q.w[j][c] = chunk(bw, (uint32_t)(j * 16 + r) * (uint32_t)a.ldw);
+                if constexpr (decltype(part)::value) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < MB; ++i) q.x[i][c] = chunk(bx, (uint32_t)(i * 16 + r) * (uint32_t)a.ldx);
+                if constexpr (decltype(part)::value) __builtin_amdgcn_sched_barrier(0);
             } else if constexpr (ODD) {
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
@@ -265,21 +269,38 @@ __global__ __launch_bounds__(kWaves * 64) void gemm_split_kernel(GemmArgs a)
     for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int i = 0; i < MB; ++i) acc[j][i] = f4zero();
+    auto multiply = [&](const Frags &q) GDN2_INLINE {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int k = 0; k < MB; ++k) acc[j][k] = Mm<T>::mma(q.w[j], q.x[k], acc[j][k]);
+    };
     const int steps = (int)((a.kbytes + kStep - 1) / kStep), mine = (steps - wv + kWaves - 1) / kWaves;
-    auto step = [&](int i) GDN2_INLINE { return wv + i * kWaves; };
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d)
-        if (d < mine) load(f[d], step(d));
-    for (int i = 0; i < mine; i += D)
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (i + d >= mine) break;
-            if (i + d + D - 1 < mine) load(f[(d + D - 1) % D], step(i + d + D - 1));
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int k = 0; k < MB; ++k) acc[j][k] = Mm<T>::mma(f[d].w[j], f[d].x[k], acc[j][k]);
+    if constexpr (D == 1 && ODD && T == Elt::kF32) {
+        // (a last step apart: in the loop its care would take the registers of a second workgroup a compute
+        // unit. 8192 x 1001 x 1001 175 us, 211 with one.)
+        const int whole = (int)(a.kbytes / kStep);
+        for (int s = wv; s < whole; s += kWaves) {
+            load(f[0], s, std::false_type{});
+            multiply(f[0]);
         }
+        if (whole < steps && whole % kWaves == wv) {
+            load(f[0], whole, std::true_type{});
+            multiply(f[0]);
+        }
+    } else {
+        auto step = [&](int i) GDN2_INLINE { return wv + i * kWaves; };
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d)
+            if (d < mine) load(f[d], step(d), std::true_type{});
+        for (int i = 0; i < mine; i += D)
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (i + d >= mine) break;
+                if (i + d + D - 1 < mine) load(f[(d + D - 1) % D], step(i + d + D - 1), std::true_type{});
+                multiply(f[d]);
+            }
+    }
 #pragma unroll
     for (int q = 0; q < ROUNDS; ++q) {
         if (q) __syncthreads();
