@@ -211,8 +211,8 @@ struct Range {
 };
 }
 
-// Whether an output shares memory with anything but its own gradient, in place; the norm
-// (written or read) and the workspace (written, or null) among them.
+// Whether an output (out: or null, the norm alone) shares memory with anything but its own gradient,
+// in place; the norm (written or read) and the workspace (written, or null) among them.
 static int clip_overlap(const void *const *grads, void *const *out, const int64_t *sizes, const int32_t *in_types,
                         const int32_t *out_types, int count, const float *norm, bool norm_given, const void *workspace, bool *bad)
 {
@@ -226,8 +226,8 @@ static int clip_overlap(const void *const *grads, void *const *out, const int64_
         auto add = [&](const void *p, int type, bool o) {
             r[n++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)sizes[i] * (type == GDN2_BF16 ? 2 : 4), i, o};
         };
-        add(out[i], out_types[i], true);
-        if (grads[i] != out[i] || in_types[i] != out_types[i]) add(grads[i], in_types[i], false);
+        if (out) add(out[i], out_types[i], true);
+        if (!out || grads[i] != out[i] || in_types[i] != out_types[i]) add(grads[i], in_types[i], false);
     }
     std::sort(r, r + n, [](const Range &a, const Range &b) { return a.begin < b.begin; });
     // (the furthest end so far of the written ranges, and of all of them)
@@ -256,14 +256,14 @@ static int clip_check(const void *const *grads, const int64_t *sizes, const int3
 int gdn2_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int count, float *norm,
                    void *workspace, size_t workspace_bytes)
 {
-    const int st = clip_check(grads, sizes, dtypes, count);
+    int st = clip_check(grads, sizes, dtypes, count);
     if (st != GDN2_OK) return st;
     if (!norm || (uintptr_t)norm % 4) return GDN2_ERR_INVALID;
     if (workspace && !aligned16(workspace)) return GDN2_ERR_INVALID;
     if (!workspace || workspace_bytes < gdn2_clip_grads_workspace_bytes()) return GDN2_ERR_WORKSPACE;
-    if (norm == workspace) return GDN2_ERR_INVALID;
-    for (int i = 0; i < count; ++i)
-        if (sizes[i] > 0 && same_memory({norm, workspace}, {grads[i]})) return GDN2_ERR_INVALID;
+    bool bad;
+    if ((st = clip_overlap(grads, nullptr, sizes, dtypes, nullptr, count, norm, false, workspace, &bad)) != GDN2_OK) return st;
+    if (bad) return GDN2_ERR_INVALID;
     ClipArgs a = {};
     a.in = grads;
     a.sizes = sizes;

@@ -601,7 +601,8 @@ int gdn2_rms_norm_bwd(const void *dy, const void *h, const float *weight, const 
  *   workspace    gdn2_clip_grads_workspace_bytes() of device memory (NULL is
  *                allowed with norm_given)
  * out[i] may be grads[i] itself with the same dtype (nothing is written there when nothing
- * is to be scaled); otherwise no out[i] may overlap any grads[j] or out[j]
+ * is to be scaled); otherwise no out[i] may overlap any grads[j], out[j] or the
+ * norm, and a norm that is written and the workspace no tensor and not each other
  * (GDN2_ERR_INVALID; checked over their whole length). Tensors lie at any
  * multiple of their element's size. Squares and their sums are fp64, in a fixed
  * order; a norm beyond the largest float is written as infinity, and scales by what

@@ -177,6 +177,11 @@ def test_clip_grads_rejects_a_norm_or_workspace_within_what_is_written(kw):
     assert clip([P, P + 0x40], [2 * P, 2 * P + 0x40], [16, 16], **kw) == INVALID
 
 
+@pytest.mark.parametrize('kw', [dict(norm=P + 4), dict(norm=P + 0x7c), dict(norm=0x200 + 64), dict(ws=P - 0x100), dict(ws=P + 0x40),
+                                dict(ws=P + 0x70), dict(grads=[2 * P, P], ws=P + 0x10)])
+def test_grad_norm_rejects_a_norm_or_workspace_within_a_gradient(kw):
+    assert norm_of(**{'grads': [P, P + 0x40], 'sizes': [16, 16], **kw}) == INVALID
+
 
 def test_binding_refuses_the_cpu_and_wrong_values():
     x, w = torch.zeros(4, 8), torch.zeros(5, 8)

@@ -170,3 +170,18 @@ def test_binding_refuses():
             (ValueError, ([g], 1.0), dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)))]:
         with pytest.raises(err):
             gdn2.clip_grads(*args, **kw)
+
+
+def test_norm_of_gradients_that_overlap():
+    """Nothing is written to them: one tensor twice, and a part of it, count as often as they are given."""
+    g = make(10, [50000], [BF])[0]
+    grads = [g, g, g[100:20000]]
+    n, tol = ref.grad_norm([back(t) for t in grads])
+    assert abs(float(gdn2.grad_norm(grads)) - n) <= tol
+
+
+def test_norm_refuses_a_workspace_within_a_gradient():
+    g = torch.ones(8192, device=DEV)
+    with pytest.raises(gdn2.Gdn2Error):
+        gdn2.grad_norm([g], workspace=g[1024:])
+    assert torch.all(g == 1)
