@@ -12,8 +12,10 @@ hipError_t launch_gemm_columns(const GemmArgs &a, hipStream_t st)
         hipLaunchKernelGGL((gemm_tile_kernel<Elt::kBf16, B, B, WM, WN, true>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, st, a,
                            (int)tm, (int)tn);
     };
+    // (the joining pass has a workgroup for 2048 elements; parts are of few tiles only, so its grid is never too large where
+    // they are asked for)
     const int64_t blocks = (a.M * ((a.N + 7) / 8) + 255) / 256;
-    if (blocks > 0xffffffLL || a.N % 8 || a.ldx % 16 || a.ldw % 16 || (a.splits > 1 && a.ldp != a.N)) return hipErrorInvalidConfiguration;
+    if (a.N % 8 || a.ldx % 16 || a.ldw % 16 || (a.splits > 1 && (a.ldp != a.N || blocks > 0xffffffLL))) return hipErrorInvalidConfiguration;
     using i2 = std::integral_constant<int, 2>;
     if (((a.M + 255) / 256) * ((a.N + 255) / 256) * a.splits >= 192)
         run(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{}, i2{});

@@ -538,9 +538,10 @@ int gdn2_layer_norm_bwd(const void *dy, const void *h, const float *weight, cons
  *
  * rows >= 0 (the gradient: up to GDN2_LINEAR_BWD_MAX_ROWS);
  * 1 <= in_features, out_features <= GDN2_LINEAR_MAX_FEATURES.
- * GDN2_ERR_UNSUPPORTED for products of two of the three sizes of about 2^37
- * and more. Pointers are 16-byte aligned; the sizes may be any number
- * (in_features in whole 16 bytes and out_features in whole eights are faster).
+ * GDN2_ERR_UNSUPPORTED, before anything is enqueued, where two of the three
+ * sizes, each rounded up to 128s, have a product of 2^37 or more. Pointers are
+ * 16-byte aligned; the sizes may be any number (in_features in whole 16 bytes
+ * and out_features in whole eights are faster).
  */
 typedef enum {
     GDN2_ACT_NONE = 0,

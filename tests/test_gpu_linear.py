@@ -426,3 +426,26 @@ def test_fp32_captured_twice(M, N, K):
         want = step()
         for out in outs:
             assert all(torch.equal(p, q) for p, q in zip(out, want)), i
+
+
+def test_weight_gradient_of_more_than_2_to_the_35_elements():
+    """64 GiB of dweight from a few rows: whole numbers, so every element has to be the exact one."""
+    M, N, K = 16, 2 ** 18, 2 ** 17 + 8
+    print(f'[weight] {M}x{N}x{K}', flush=True)
+    torch.cuda.empty_cache()
+    g = torch.Generator(device=DEV).manual_seed(16)
+    dy = torch.randint(-1, 2, (M, N), generator=g, device=DEV).bfloat16()
+    x = torch.randint(-8, 9, (M, K), generator=g, device=DEV).bfloat16()
+    # (sums of at most 128: whole numbers that bf16 holds)
+    dw = torch.empty(N, K, dtype=torch.bfloat16, device=DEV)
+    lib, code = gdn2.lib(), gdn2.GDN2_BF16
+    need = lib.gdn2_linear_bwd_workspace_bytes(M, K, N, 0, code, code, 0, 1, 0)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    lib.gdn2_set_stream(torch.cuda.current_stream().cuda_stream)
+    assert lib.gdn2_linear_bwd(dy.data_ptr(), x.data_ptr(), None, None, None, dw.data_ptr(), None, M, K, N, 0, code, code, ws.data_ptr(),
+                               need) == gdn2.GDN2_OK
+    xf = x.float()
+    for n in range(0, N, 8192):
+        assert torch.equal(dw[n:n + 8192], (dy[:, n:n + 8192].float().t().contiguous() @ xf).bfloat16()), n
+    del dw
+    torch.cuda.empty_cache()
