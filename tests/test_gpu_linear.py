@@ -449,3 +449,28 @@ def test_weight_gradient_of_more_than_2_to_the_35_elements():
         assert torch.equal(dw[n:n + 8192], (dy[:, n:n + 8192].float().t().contiguous() @ xf).bfloat16()), n
     del dw
     torch.cuda.empty_cache()
+
+
+# blocks of the waves that share the contraction, tiles, rows that are no whole chunks
+@pytest.mark.parametrize('M,N,K', [(24, 48, 96), (700, 4096, 64), (2000, 1001, 33)])
+def test_scales_whose_product_leaves_the_range(M, N, K):
+    """x has one element a row, so z is one exact product v times two scales; each of the scales' products
+    overflows or vanishes somewhere while v times both does not."""
+    g = torch.Generator().manual_seed(17)
+    x = torch.zeros(M, K)
+    x[torch.arange(M), torch.arange(M) % K] = torch.randint(-8, 9, (M,), generator=g).float() * 2.0 ** torch.randint(-6, 5, (M,), generator=g)
+    w = torch.randint(-8, 9, (N, K), generator=g).float() * 2.0 ** -6
+    far = torch.tensor([1.0, 1e25, 1e-25, 1e30, 1e-30, 3e38, 1e-38, 1e-42, 0.0])
+    mant = lambda n: 1 + torch.rand(n, generator=g) / 9   # noqa: E731
+    sx, sw = far[torch.randint(0, 9, (M,), generator=g)] * mant(M), far[torch.randint(0, 9, (N,), generator=g)] * mant(N)
+    e, d = lambda t: t.to(DT['e4m3']).to(DEV), lambda t: t.to(DEV)   # noqa: E731
+    assert np.array_equal(back(e(x)), x.numpy()) and np.array_equal(back(e(w)), w.numpy())
+    y, _ = gdn2.linear_fwd(e(x), e(w), x_scale=d(sx), weight_scale=d(sw), out_dtype=torch.float32)
+    v = x.double() @ w.double().t()
+    want = (v * sx.double()[:, None] * sw.double()).numpy()
+    got = back(y).astype(np.float64)
+    # (v, both mantissas' product and v's with it are rounded, and the result; its exponent may leave the range itself)
+    inside = np.abs(want) < 3.4e38
+    assert np.all(np.abs(got - want)[inside] <= 4 * oref.U * np.abs(want)[inside] + 2.0 ** -149)
+    assert np.all(np.isinf(got[np.abs(want) > 3.41e38]))
+    assert inside.mean() > 0.5 and np.any((want != 0) & inside & ~np.isfinite((sx[:, None] * sw).numpy()))
