@@ -117,10 +117,26 @@ __global__ __launch_bounds__(kThreads) void clip_finish_kernel(const double *par
     if (threadIdx.x == 0) *norm = (float)x;
 }
 
+// What the gradients are multiplied by, as a normal number and a power of two (2^0 but for quotients below those:
+// a large gradient times such a one is an ordinary float). Beside a plain product: 206 M bf16 to fp32 286.2 us and
+// 285.8, 7 M floats 20.9 and 20.5.
+struct Factor {
+    float m;
+    int e;
+    __device__ __forceinline__ explicit Factor(double q)   // (NaN stays)
+    {
+        const bool small = q < 0x1p-126;
+        m = q >= 1. ? 1.f : (float)(small ? __builtin_amdgcn_frexp_mant(q) : q);
+        e = small ? __builtin_amdgcn_frexp_exp(q) : 0;
+    }
+    __device__ __forceinline__ float operator()(float x) const { return __builtin_amdgcn_ldexpf(x * m, e); }
+    __device__ __forceinline__ bool one() const { return m == 1.f && e == 0; }
+};
+
 // n elements of p (kPiece at most) to o, times c. A lane takes eight neighbours at a time, or four where one
 // side is fp32, so that a wave's loads and stores are each in one piece.
 template <bool CACHED, typename In, typename Out>
-static __device__ __forceinline__ void piece_scale(const In *p, Out *o, int64_t n, float c)
+static __device__ __forceinline__ void piece_scale(const In *p, Out *o, int64_t n, Factor c)
 {
     constexpr int V = sizeof(In) + sizeof(Out) > 4 ? 4 : 8, R = 2;   // rounds whose loads are under way at once
     typedef uint32_t vin __attribute__((ext_vector_type(V * sizeof(In) / 4)));
@@ -150,12 +166,12 @@ static __device__ __forceinline__ void piece_scale(const In *p, Out *o, int64_t 
                 vout y;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    if constexpr (sizeof(Out) == 4) y[i] = __float_as_uint(get(x[r], i) * c);
-                    else if (i % 2 == 0) y[i / 2] = bf16x2(get(x[r], i) * c, get(x[r], i + 1) * c);
+                    if constexpr (sizeof(Out) == 4) y[i] = __float_as_uint(c(get(x[r], i)));
+                    else if (i % 2 == 0) y[i / 2] = bf16x2(c(get(x[r], i)), c(get(x[r], i + 1)));
                 }
                 __builtin_nontemporal_store(y, reinterpret_cast<vout_any *>(o + at));
             } else {
-                for (int i = at; i < n && i < at + V; ++i) store1(o + i, in2f<In>(p[i]) * c);
+                for (int i = at; i < n && i < at + V; ++i) store1(o + i, c(in2f<In>(p[i])));
             }
         }
     }
@@ -169,12 +185,11 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipBatch b, const
     // (a norm beyond the largest float still scales by what it is)
     const double norm = norm_in ? (double)*norm_in : norm_of(partial, parts, red);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-    const double q = (double)max_norm / (norm + 1e-6);
-    const float c = q >= 1. ? 1.f : (float)q;   // (NaN stays)
+    const Factor c((double)max_norm / (norm + 1e-6));
     for (int i = blockIdx.x; i < b.pieces; i += gridDim.x) {
         const int p = b.pieces - 1 - i, t = tensor_of(b, p);
         const int64_t at = (int64_t)(p - b.first[t]) * kPiece, n = b.n[t] - at;
-        if (c == 1.f && b.in[t] == b.out[t]) continue;   // nothing to change
+        if (c.one() && b.in[t] == b.out[t]) continue;   // nothing to change
         const bool ib = (b.in_bf16 >> t) & 1, ob = (b.out_bf16 >> t) & 1;
         if (ib) {
             const uint16_t *x = (const uint16_t *)b.in[t] + at;

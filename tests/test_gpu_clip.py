@@ -185,3 +185,12 @@ def test_norm_refuses_a_workspace_within_a_gradient():
     with pytest.raises(gdn2.Gdn2Error):
         gdn2.grad_norm([g], workspace=g[1024:])
     assert torch.all(g == 1)
+
+
+@pytest.mark.parametrize('max_norm', [1e-3, 1e-6, 1e-30, 1e-37])
+@pytest.mark.parametrize('types', [[F, F], [BF, F]])
+def test_factors_below_the_smallest_float(types, max_norm):
+    """Gradients near the range's end and a small largest norm: their quotient is no normal number, the results are."""
+    check(make(11, [3000, 17], types, 3e37), max_norm)
+    grads = make(12, [20000, 33], types, 1e37)
+    check(grads, max_norm, [torch.zeros_like(g, dtype=F) for g in grads])
