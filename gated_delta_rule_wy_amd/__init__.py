@@ -923,7 +923,8 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     """act(x weight^T + bias) + residual (gdn2_linear_fwd). x: [..., in_features],
     weight: [out_features, in_features], one dtype: bf16, fp32, or float8_e4m3fn
     with fp32 x_scale ([...], x's leading shape) and weight_scale [out_features],
-    which multiply the product. bias: [out_features] fp32. residual:
+    which multiply the product (large ones to bf16 are added with fewer bits than
+    fp32's, see gdn2.h; to fp32 they are not). bias: [out_features] fp32. residual:
     [..., out_features] in the output's dtype. activation: None, 'sigmoid',
     'silu' or 'gelu_tanh'. Returns (y in ``out_dtype`` (None: x's; bf16 for 8 bits),
     z or None): z, the activation's argument in x's dtype, is what ``linear_bwd``

@@ -50,7 +50,8 @@ constexpr int kClipGrid = 1024;  // most workgroups of its kernels
 hipError_t launch_clip(const ClipArgs &a, hipStream_t st);
 
 // Products with both operands' contracted axis along their rows (linear_impl.hpp).
-enum class Elt { kBf16, kF32, kE4m3 };
+// (kE4m3Wide: e4m3 operands that are widened to bf16 in registers; launches name kE4m3)
+enum class Elt { kBf16, kF32, kE4m3, kE4m3Wide };
 enum Act { kActNone = 0, kActSigmoid = 1, kActSilu = 2, kActGelu = 3 };
 inline int elt_size(Elt e) { return e == Elt::kBf16 ? 2 : e == Elt::kF32 ? 4 : 1; }
 

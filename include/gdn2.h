@@ -520,10 +520,11 @@ int gdn2_layer_norm_bwd(const void *dy, const void *h, const float *weight, cons
  * act: none, sigmoid, silu z sigmoid(z), or gelu in its tanh form
  *   0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))).
  * e4m3 is the 8-bit float with 4 exponent and 3 mantissa bits, no infinities
- * and largest value 448. Products are exact and sums fp32, in a fixed order; of
- * e4m3 products, aligned eights along k are first added with 13 bits below the
- * largest of them (the matrix instruction's way: an error of up to 2^-13 of it
- * for each of the others).
+ * and largest value 448. Products are exact and sums fp32, in a fixed order. Of
+ * e4m3 products whose y is bf16, large ones (about 2^20 elements of y and more)
+ * are added in aligned eights along k, with 13 bits below the largest of the eight
+ * (the matrix instruction's way at its full rate: an error of up to 2^-13 of it
+ * for each of the others); with y in fp32 all sums are fp32, at half the rate.
  * Otherwise no output overlaps an input or another output (GDN2_ERR_INVALID
  * where two pointers are one; partial overlaps are not checked).
  *

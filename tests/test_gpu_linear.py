@@ -474,3 +474,61 @@ def test_scales_whose_product_leaves_the_range(M, N, K):
     assert np.all(np.abs(got - want)[inside] <= 4 * oref.U * np.abs(want)[inside] + 2.0 ** -149)
     assert np.all(np.isinf(got[np.abs(want) > 3.41e38]))
     assert inside.mean() > 0.5 and np.any((want != 0) & inside & ~np.isfinite((sx[:, None] * sw).numpy()))
+
+
+# e4m3 sums: one form of the blocks of waves that share the contraction each (16 x 16 to 32 x 64), tiles of each
+# size, rows that are no whole chunks in both kinds
+SUMS = [(20, 48, 96), (20, 4096, 300 * 16), (60, 4096, 2048), (100, 2048, 512), (256, 2048, 1040), (300, 257, 1000), (1000, 2056, 528),
+        (4000, 1024, 272), (5000, 2048, 272), (2000, 1001, 333)]
+
+
+def check_sums(M, N, K, out):
+    """Whole numbers whose every sum, in whatever order, is one below 2^24: 2^16 twice in an aligned eight, which
+    cancel, beside products of at most 9. fp32 holds all of it, so the result has to be exact."""
+    g = torch.Generator().manual_seed(18)
+    x, w = torch.randint(-3, 4, (M, K), generator=g).float(), torch.randint(-3, 4, (N, K), generator=g).float()
+    at = torch.arange(0, K - 1, 8)
+    at = at[torch.randperm(len(at), generator=g)[:96]]
+    x[:, at], x[:, at + 1] = 256.0, 256.0
+    w[:, at], w[:, at + 1] = 256.0, -256.0
+    want = (x.double() @ w.double().t()).float()
+    d, one = lambda t: t.to(DT['e4m3']).to(DEV), lambda n: torch.ones(n, device=DEV)   # noqa: E731
+    y, _ = gdn2.linear_fwd(d(x), d(w), x_scale=one(M), weight_scale=one(N), out_dtype=DT[out])
+    assert torch.equal(y.cpu(), want.to(DT[out]))
+
+
+@pytest.mark.parametrize('M,N,K', SUMS)
+def test_sums_of_8_bit_products(M, N, K):
+    print(f'[sums] {M}x{N}x{K}', flush=True)
+    check_sums(M, N, K, 'f32')
+
+
+# (those that are no tiles)
+@pytest.mark.parametrize('M,N,K', [s for s in SUMS if s[0] <= 300 or s[1] % 8])
+def test_sums_of_8_bit_products_in_blocks(M, N, K):
+    """Where the matrix instructions' rate is no bound the bf16 output has them too."""
+    print(f'[sums] {M}x{N}x{K}', flush=True)
+    check_sums(M, N, K, 'bf16')
+
+
+@pytest.mark.parametrize('rows', [3, 5000])
+@pytest.mark.parametrize('N,K', [(256, 256), (257, 256)])
+def test_every_8_bit_number(rows, N, K):
+    """Each of the 256 codes on either side of a one."""
+    codes = torch.arange(256, dtype=torch.uint8).view(DT['e4m3'])
+    want = codes.float()
+    hot = torch.zeros(rows, K)
+    hot[:, 0] = 1
+    w = torch.zeros(N, K, dtype=torch.uint8)
+    w[:256, 0] = torch.arange(256, dtype=torch.uint8)
+    one = lambda n: torch.ones(n, device=DEV)   # noqa: E731
+    run = lambda x, w: gdn2.linear_fwd(x, w, x_scale=one(len(x)), weight_scale=one(len(w)), out_dtype=torch.float32)[0]   # noqa: E731
+    y = run(hot.to(DT['e4m3']).to(DEV), w.view(DT['e4m3']).to(DEV)).cpu()
+    assert torch.equal(torch.nan_to_num(y[:, :256], 999.0), torch.nan_to_num(want, 999.0).expand(rows, 256))
+    x = torch.zeros(rows, K, dtype=torch.uint8)
+    at = torch.arange(rows) % 256
+    x[:, 0] = at.to(torch.uint8)
+    hot = torch.zeros(N, K)
+    hot[:, 0] = 1
+    y = run(x.view(DT['e4m3']).to(DEV), hot.to(DT['e4m3']).to(DEV)).cpu()
+    assert torch.equal(torch.nan_to_num(y, 999.0), torch.nan_to_num(want[at], 999.0)[:, None].expand(rows, N))
