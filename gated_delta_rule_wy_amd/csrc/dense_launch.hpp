@@ -46,7 +46,7 @@ struct ClipArgs {
     float *norm_out;             // or null
     double *partial;             // [kClipGrid]
 };
-constexpr int kClipGrid = 1024;  // most workgroups of its kernels
+constexpr int kClipGrid = 1024;  // most workgroups of the norm, and partial sums
 hipError_t launch_clip(const ClipArgs &a, hipStream_t st);
 
 // Products with both operands' contracted axis along their rows (linear_impl.hpp).

@@ -52,7 +52,7 @@ struct TurnArgs {
     const void *in;        // [R][C]
     const void *preact;    // [R][C], type of the outputs; null: in itself is what is turned
     void *copy;            // [R][Cp] or null
-    void *turned;          // [C][Rp] or null
+    void *turned;          // [C][Rp]; null: dz_kernel takes it
     float *partial;        // [gridDim.y][C] column sums, or null
     int64_t R, Rp;
     int C, Cp, act;
@@ -94,25 +94,22 @@ template <typename In, typename T> __global__ __launch_bounds__(256) void turn_k
                 db[i] += v[i];
             }
             if (a.copy && r < a.R && c < a.Cp) store8<true>((T *)a.copy + r * a.Cp + c, v);
-            if (a.turned)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) store1(&tile[h * 32 + row][p * 8 + i], v[i]);
+            for (int i = 0; i < 8; ++i) store1(&tile[h * 32 + row][p * 8 + i], v[i]);
         }
-        if (a.turned) {
-            __syncthreads();
+        __syncthreads();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int tc = h * 32 + row;     // column of the tile, row of the outcome
-                const int64_t r = r0 + p * 8;
-                if (c0 + tc < a.C && r < a.Rp) {
-                    float v[8];
+        for (int h = 0; h < 2; ++h) {
+            const int tc = h * 32 + row;     // column of the tile, row of the outcome
+            const int64_t r = r0 + p * 8;
+            if (c0 + tc < a.C && r < a.Rp) {
+                float v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = in2f<T>(tile[p * 8 + i][tc]);
-                    store8<true>((T *)a.turned + (int64_t)(c0 + tc) * a.Rp + r, v);
-                }
+                for (int i = 0; i < 8; ++i) v[i] = in2f<T>(tile[p * 8 + i][tc]);
+                store8<true>((T *)a.turned + (int64_t)(c0 + tc) * a.Rp + r, v);
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
     if (a.partial) {
 #pragma unroll
@@ -356,10 +353,11 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a, hipStream_t st)
 
 // ---- the choice of a product's form ---------------------------------------------
 
-int gemm_splits(int64_t M, int64_t N, int64_t kbytes)
+// (rows x cols: the smaller tiles that a product of few of them takes)
+static int splits_of(int64_t M, int64_t N, int64_t kbytes, int rows, int cols)
 {
     auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-    const int64_t steps = (kbytes + 127) / 128, big = tiles(256, 256), small = tiles(128, 64);
+    const int64_t steps = (kbytes + 127) / 128, big = tiles(256, 256), small = tiles(rows, cols);
     if (M == 0 || big >= 192) return 1;
     // one part a compute unit, each of 16 steps at least
     int64_t s = std::min((256 + big - 1) / big, steps / 16);
@@ -367,17 +365,8 @@ int gemm_splits(int64_t M, int64_t N, int64_t kbytes)
     s = std::min((512 + small - 1) / small, steps / 16);
     return s >= 2 ? (int)s : 1;
 }
-
-int gemm_columns_splits(int64_t M, int64_t N, int64_t kbytes)
-{
-    auto tiles = [&](int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
-    const int64_t steps = (kbytes + 127) / 128, big = tiles(256), small = tiles(128);
-    if (big >= 192) return 1;
-    int64_t s = std::min((256 + big - 1) / big, steps / 16);
-    if (s >= 1 && big * s >= 192) return (int)s;
-    s = std::min((512 + small - 1) / small, steps / 16);
-    return s >= 2 ? (int)s : 1;
-}
+int gemm_splits(int64_t M, int64_t N, int64_t kbytes) { return splits_of(M, N, kbytes, 128, 64); }
+int gemm_columns_splits(int64_t M, int64_t N, int64_t kbytes) { return splits_of(M, N, kbytes, 128, 128); }
 
 bool gemm_columns_f32(int64_t M, int64_t N, int64_t count, bool turned_x)
 {
