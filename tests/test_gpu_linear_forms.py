@@ -134,3 +134,22 @@ def test_gradient_with_nothing_beyond_the_tensors(M, N, K, dtype, act):
         same(f'd{n}', out[n][:t.numel()].view(t.shape), t)
         assert torch.all(out[n][t.numel():] == 7.0)
     assert torch.all(ws[need:] == 0xff)
+
+
+# the most features that are taken, and one fewer
+@pytest.mark.parametrize('dtype', ['bf16', 'f32', 'e4m3'])
+@pytest.mark.parametrize('M,N,K', [(1, 48, 2 ** 20), (300, 40, 2 ** 20 - 1), (600, 520, 2 ** 20), (700, 257, 2 ** 20 - 1), (33, 2 ** 20, 40),
+                                   (1, 2 ** 20 - 1, 33), (300, 2 ** 20, 16)])
+def test_the_most_features(M, N, K, dtype):
+    print(f'[features] {M}x{N}x{K} {dtype}', flush=True)
+    x, w = whole(M, 3, M, K), whole(N, 3, N, K)
+    want = torch.cat([x.double() @ w[n:n + 65536].double().t() for n in range(0, N, 65536)], 1).float()
+    scale = dict(x_scale=torch.ones(M, device=DEV), weight_scale=torch.ones(N, device=DEV)) if dtype == 'e4m3' else {}
+    y, _ = gdn2.linear_fwd(x.to(DT[dtype]), w.to(DT[dtype]), out_dtype=torch.float32, **scale)
+    same('y', y, want)
+
+
+@pytest.mark.parametrize('dtype', ['bf16', 'f32'])
+@pytest.mark.parametrize('M,N,K', [(64, 2 ** 20, 16), (70, 24, 2 ** 20), (33, 2 ** 20 - 1, 9), (40, 9, 2 ** 20 - 1)])
+def test_gradient_of_the_most_features(M, N, K, dtype):
+    gradient(M, N, K, dtype, 3, 2)
