@@ -418,8 +418,8 @@ static __device__ __forceinline__ int swap_of(int row) { return (row >> 1) & 7; 
 // Workgroups stay and go through the tiles; the last two steps of a tile bring
 // the first two of the next, so the sums' way to memory overlaps with them.
 //
-// 65536 x 2048 x 2048 bf16 490 us, with residual 535 (1.03 PFLOP/s); 32768 x 8192 x 2048 e4m3 to bf16 505 (2.18); by
-// columns 2048 x 2048 x 32768 bf16 290 (0.95). A tile of 256 x 256 and 2048 bf16 takes 60 us of its compute unit, 37 in matrix
+// 65536 x 2048 x 2048 bf16 490 us, with residual 528 (1.04 PFLOP/s); 32768 x 8192 x 2048 e4m3 to bf16 511 to 522 (2.1); by
+// columns 2048 x 2048 x 32768 bf16 298 (0.92). A tile of 256 x 256 and 2048 bf16 takes 60 us of its compute unit, 37 in matrix
 // instructions alone, 49 with the reads of LDS, and 49 in fetches alone (33 where the L2 has all): x comes from memory
 // behind the bursts in which y leaves.
 

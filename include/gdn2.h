@@ -574,7 +574,8 @@ int gdn2_linear_bwd(const void *dy, const void *x, const void *weight, const voi
  *                gdn2_linear_fwd takes with this x_scale
  * y (same type) and sum may each be x or residual itself, but must not overlap
  * an input otherwise, nor each other (GDN2_ERR_INVALID where they are one). The
- * squares of a row are added in fp32: above about 1e19 their sum is infinite.
+ * squares of a row are added in fp32: above about 1e19 their sum is infinite. A
+ * NaN in h makes its row NaN; scale is then that of a row of zeros.
  *
  * gdn2_rms_norm_bwd: as gdn2_layer_norm_bwd, without a bias; dy is dL/dy in
  * out_dtype, GDN2_F32 or GDN2_BF16.

@@ -236,3 +236,19 @@ def test_binding_refuses():
                           (ValueError, (x, x, w), dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)))]:
         with pytest.raises(err):
             gdn2.rms_norm_bwd(*args, **kw)
+
+
+@pytest.mark.parametrize('cols', [5, 64, 2048, 2049, 5000, 20000])
+@pytest.mark.parametrize('dtype', [torch.bfloat16, torch.float32])
+def test_not_a_number_stays_in_its_row(cols, dtype):
+    """In 8 bits with the least scale."""
+    g = torch.Generator().manual_seed(cols)
+    x, w = torch.randn(9, cols, generator=g).to(dtype).to(DEV), torch.ones(cols, device=DEV)
+    e4m3 = torch.float8_e4m3fn
+    y0, _, s0 = gdn2.rms_norm_fwd(x, w, out_dtype=e4m3)
+    x[4, cols // 2] = float('nan')
+    y, _, s = gdn2.rms_norm_fwd(x, w, out_dtype=e4m3)
+    others = [r for r in range(9) if r != 4]
+    assert torch.equal(y.view(torch.uint8)[others], y0.view(torch.uint8)[others]) and torch.equal(s[others], s0[others])
+    assert torch.all(torch.isnan(y[4].float())) and float(s[4]) == 2.0 ** -126
+    assert torch.all(torch.isnan(gdn2.rms_norm_fwd(x, w)[0][4].float()))
